@@ -11,6 +11,7 @@ Names follow the C ABI: ``nf4_quantize``, ``nf4_dequantize``,
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -31,7 +32,8 @@ EXPORTS = ("qlora_nf4_sizes", "nf4_quantize", "nf4_quantize_noalloc", "nf4_dequa
            "qlora_profile_enable", "qlora_profile_read",
            "qlora_dropout_mask", "qlora_linear_dropout_workspace_size", "qlora_linear_fwd_dropout",
            "qlora_linear_bwd_dropout", "qlora_selftest_wait_timeout", "qlora_grouped_workspace_size",
-           "qlora_linear_fwd_grouped", "qlora_linear_bwd_grouped")
+           "qlora_linear_fwd_grouped", "qlora_linear_bwd_grouped",
+           "qlora_layer_norm_fwd", "qlora_layer_norm_bwd", "qlora_layer_norm_workspace_size")
 
 KERNEL_CLASSES = ("quant", "dq_const", "dequant", "fwd_gemm", "bwd_gemm", "lora_gemm", "aux")
 
@@ -61,6 +63,12 @@ class QloraDropout(ctypes.Structure):
     """Mirror of ``qlora_dropout_t``: adapter dropout probability p and the
     generator's (seed, offset)."""
     _fields_ = [("p", ctypes.c_float), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64)]
+
+
+class QloraNorm(ctypes.Structure):
+    """Mirror of ``qlora_norm_t``."""
+    _fields_ = [("M", ctypes.c_int64), ("D", ctypes.c_int64), ("dtype", ctypes.c_int32), ("wdtype", ctypes.c_int32),
+                ("rms", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -101,6 +109,10 @@ def lib() -> ctypes.CDLL:
     L.qlora_linear_fwd_grouped.argtypes = [vp, c_i64, G, vp, vp, c_i32, ctypes.c_float, vp, vp, vp, c_sz, vp]
     L.qlora_linear_bwd_grouped.argtypes = [vp, vp, c_i64, G, vp, vp, c_i32, ctypes.c_float, vp, vp, vp, vp, vp,
                                            c_sz, vp]
+    NP = ctypes.POINTER(QloraNorm)
+    L.qlora_layer_norm_fwd.argtypes = [NP, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.qlora_layer_norm_bwd.argtypes = [NP, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, c_sz, vp]
+    L.qlora_layer_norm_workspace_size.argtypes = [NP, c_i32, ctypes.POINTER(c_sz)]
     L.qlora_last_error.restype = ctypes.c_char_p
     L.qlora_profile_enable.argtypes = [c_i32]
     L.qlora_profile_read.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64)]
@@ -110,7 +122,8 @@ def lib() -> ctypes.CDLL:
                  "qlora_profile_enable", "qlora_profile_read", "qlora_dropout_mask",
                  "qlora_linear_dropout_workspace_size", "qlora_linear_fwd_dropout", "qlora_linear_bwd_dropout",
                  "qlora_selftest_wait_timeout", "qlora_grouped_workspace_size", "qlora_linear_fwd_grouped",
-                 "qlora_linear_bwd_grouped"):
+                 "qlora_linear_bwd_grouped", "qlora_layer_norm_fwd", "qlora_layer_norm_bwd",
+                 "qlora_layer_norm_workspace_size"):
         getattr(L, name).restype = c_i32
     _lib = L
     return L
@@ -568,6 +581,127 @@ def qlora_linear_bwd(dY: torch.Tensor, X: torch.Tensor, q: NF4Weight, A: torch.T
                                               dA.data_ptr(), dB.data_ptr(), _ptr(workspace), _nbytes(workspace),
                                               _stream(stream)))
     return dX, dA, dB
+
+
+# ---------------------------------------------------------------------------
+# the operators around the linear layer in a fine-tuning step
+# ---------------------------------------------------------------------------
+_DT = {torch.bfloat16: 0, torch.float32: 1}     # QLORA_DT_*
+
+
+def _dt(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in _DT:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.bfloat16 or torch.float32")
+    return _DT[t.dtype]
+
+
+def _on_cuda(t: torch.Tensor, name: str) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device, is on {t.device}")
+    return t.device
+
+
+def _enter(dev: torch.device, stream):
+    """(raw stream, context for the call's own allocations): the current stream
+    of the tensors' device, or the caller's stream, which then also owns what
+    the call allocates."""
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream, contextlib.nullcontext()
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the call runs on {dev}")
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def _norm_struct(X: torch.Tensor, weight: torch.Tensor, name: str, rms: bool, eps: float) -> QloraNorm:
+    if X.dim() != 2:
+        raise ValueError(f"{name}: shape {tuple(X.shape)}, expected (rows, values)")
+    return QloraNorm(X.shape[0], X.shape[1], _dt(X, name), _dt(weight, "weight"), int(bool(rms)), float(eps))
+
+
+def qlora_layer_norm_fwd(X: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                         residual: Optional[torch.Tensor] = None, eps: float = 1e-5, rms: bool = False,
+                         Y: Optional[torch.Tensor] = None, S: Optional[torch.Tensor] = None,
+                         mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None, stream=None):
+    """S = X + residual; Y = (S - mean) rstd weight + bias over each row of a
+    bf16 or fp32 (M, D) tensor (rms: no mean is subtracted).  Returns
+    (Y, S, mean, rstd) for qlora_layer_norm_bwd; S is X without a residual and
+    mean is None for rms.  Y and S may be X or residual (in place)."""
+    n = _norm_struct(X, weight, "X", rms, eps)
+    M, D = X.shape
+    _expect(X, "X", (M, D), X.dtype)
+    _expect(residual, "residual", (M, D), X.dtype, required=False)
+    _expect(weight, "weight", (D,), weight.dtype)
+    _expect(bias, "bias", (D,), weight.dtype, required=False)
+    if S is not None and residual is None:
+        raise ValueError("S goes with residual")
+    if mean is not None and rms:
+        raise ValueError("mean is not used with rms")
+    for t, name, shape, dtype in ((Y, "Y", (M, D), X.dtype), (S, "S", (M, D), X.dtype),
+                                  (mean, "mean", (M,), torch.float32), (rstd, "rstd", (M,), torch.float32)):
+        _expect(t, name, shape, dtype, required=False)
+    dev = _on_cuda(X, "X")
+    _same_device(dev, residual=residual, weight=weight, bias=bias, Y=Y, S=S, mean=mean, rstd=rstd)
+    raw, own = _enter(dev, stream)
+    with own:
+        if Y is None:
+            Y = torch.empty_like(X)
+        if S is None and residual is not None:
+            S = torch.empty_like(X)
+        if mean is None and not rms:
+            mean = torch.empty(M, dtype=torch.float32, device=dev)
+        if rstd is None:
+            rstd = torch.empty(M, dtype=torch.float32, device=dev)
+    _check(lib().qlora_layer_norm_fwd(ctypes.byref(n), X.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias),
+                                      _ptr(S), Y.data_ptr(), _ptr(mean), rstd.data_ptr(), raw))
+    return Y, (X if S is None else S), mean, rstd
+
+
+def qlora_layer_norm_workspace_size(M: int, D: int, dtype=torch.bfloat16, with_dbias: bool = False) -> int:
+    n = ctypes.c_size_t()
+    st = QloraNorm(M, D, _DT[dtype], 1, 0, 0.0)
+    _check(lib().qlora_layer_norm_workspace_size(ctypes.byref(st), int(with_dbias), ctypes.byref(n)))
+    return n.value
+
+
+def qlora_layer_norm_bwd(dY: torch.Tensor, S: torch.Tensor, weight: torch.Tensor, mean: Optional[torch.Tensor],
+                         rstd: torch.Tensor, dS: Optional[torch.Tensor] = None, rms: bool = False,
+                         dX: Optional[torch.Tensor] = None, dweight: Optional[torch.Tensor] = None,
+                         dbias: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                         stream=None, need_dbias: bool = False):
+    """Backward of qlora_layer_norm_fwd; returns (dX, dweight, dbias).  dX is
+    the gradient of X and of the residual alike; dS is the gradient that
+    reaches S along the residual stream.  dweight and dbias are fp32; dbias is
+    computed with need_dbias or where a tensor for it is given."""
+    n = _norm_struct(S, weight, "S", rms, 0.0)
+    M, D = S.shape
+    f32 = torch.float32
+    _expect(S, "S", (M, D), S.dtype)
+    _expect(dY, "dY", (M, D), S.dtype)
+    _expect(weight, "weight", (D,), weight.dtype)
+    _expect(mean, "mean", (M,), f32, required=not rms)
+    _expect(rstd, "rstd", (M,), f32)
+    for t, name, shape, dtype in ((dS, "dS", (M, D), S.dtype), (dX, "dX", (M, D), S.dtype),
+                                  (dweight, "dweight", (D,), f32), (dbias, "dbias", (D,), f32)):
+        _expect(t, name, shape, dtype, required=False)
+    dev = _on_cuda(S, "S")
+    _same_device(dev, dY=dY, weight=weight, mean=mean, rstd=rstd, dS=dS, dX=dX, dweight=dweight, dbias=dbias,
+                 workspace=workspace)
+    raw, own = _enter(dev, stream)
+    with own:
+        if dX is None:
+            dX = torch.empty_like(S)
+        if dweight is None:
+            dweight = torch.empty(D, dtype=f32, device=dev)
+        if dbias is None and need_dbias:
+            dbias = torch.empty(D, dtype=f32, device=dev)
+        if workspace is None:
+            with torch.cuda.device(dev):
+                nws = qlora_layer_norm_workspace_size(M, D, S.dtype, dbias is not None)
+            workspace = torch.empty(max(nws, 16), dtype=torch.uint8, device=dev)
+    _check(lib().qlora_layer_norm_bwd(ctypes.byref(n), dY.data_ptr(), S.data_ptr(), weight.data_ptr(),
+                                      None if rms else mean.data_ptr(), rstd.data_ptr(), _ptr(dS), dX.data_ptr(),
+                                      dweight.data_ptr(), _ptr(dbias), workspace.data_ptr(), _nbytes(workspace), raw))
+    return dX, dweight, dbias
 
 
 def qlora_nf4_codebook():

@@ -538,6 +538,106 @@ int qlora_lora_merge(const qlora_nf4_t* q, const uint16_t* A, const uint16_t* B,
                     "qlora_lora_merge launch");
 }
 
+}  // extern "C"
+
+// The entry points around the linear layer restore the calling thread's device.
+namespace {
+struct DeviceScope {
+  int prev = -1;
+  int bind(const void* p) {
+    if (cudaGetDevice(&prev) != cudaSuccess) {
+      cudaGetLastError();
+      prev = -1;
+    }
+    return bind_device(p);
+  }
+  ~DeviceScope() {
+    int now = prev;
+    if (prev >= 0 && cudaGetDevice(&now) == cudaSuccess && now != prev) cudaSetDevice(prev);
+  }
+};
+}  // namespace
+
+static int check_ptr4(const void* p, const char* name, bool required) {
+  if (!p) return required ? fail(QLORA_ERR_INVALID_ARG, "%s is NULL", name) : ok();
+  if (!aligned(p, 4)) return fail(QLORA_ERR_ALIGNMENT, "%s must be 4-byte aligned", name);
+  return ok();
+}
+
+static int check_norm(const qlora_norm_t* n) {
+  if (!n) return fail(QLORA_ERR_INVALID_ARG, "norm descriptor is NULL");
+  if (n->M < 0 || n->D < 1) return fail(QLORA_ERR_INVALID_ARG, "bad shape M=%lld D=%lld", (long long)n->M, (long long)n->D);
+  if (n->D > kNormMaxDim) return fail(QLORA_ERR_UNSUPPORTED, "D=%lld above %lld", (long long)n->D, (long long)kNormMaxDim);
+  if (n->M > (int64_t(1) << 31)) return fail(QLORA_ERR_UNSUPPORTED, "M=%lld above 2^31", (long long)n->M);
+  if (n->dtype < 0 || n->dtype > 1 || n->wdtype < 0 || n->wdtype > 1)
+    return fail(QLORA_ERR_INVALID_ARG, "dtype and wdtype must be QLORA_DT_BF16 or QLORA_DT_F32");
+  if (!(n->eps >= 0.0f)) return fail(QLORA_ERR_INVALID_ARG, "eps must be >= 0");
+  return QLORA_OK;
+}
+
+static NormArgs norm_args(const qlora_norm_t* n) {
+  NormArgs a{};
+  a.M = n->M; a.D = static_cast<int>(n->D); a.dtype = n->dtype; a.wdtype = n->wdtype; a.rms = n->rms != 0; a.eps = n->eps;
+  return a;
+}
+
+extern "C" {
+
+int qlora_layer_norm_fwd(const qlora_norm_t* n, const void* X, const void* R, const void* weight, const void* bias,
+                         void* S, void* Y, float* mean, float* rstd, qlora_stream_t stream) {
+  int rc = check_norm(n);
+  if (rc) return rc;
+  if (n->M == 0) return ok();
+  if ((R == nullptr) != (S == nullptr)) return fail(QLORA_ERR_INVALID_ARG, "S goes with R: both or neither");
+  if ((rc = check_ptr16(X, "X", true)) || (rc = check_ptr16(R, "R", false)) ||
+      (rc = check_ptr16(weight, "weight", true)) || (rc = check_ptr16(bias, "bias", false)) ||
+      (rc = check_ptr16(S, "S", false)) || (rc = check_ptr16(Y, "Y", true)) ||
+      (rc = check_ptr4(mean, "mean", false)) || (rc = check_ptr4(rstd, "rstd", false)))
+    return rc;
+  DeviceScope scope;
+  if ((rc = scope.bind(X))) return rc;
+  NormArgs a = norm_args(n);
+  a.X = X; a.R = R ? R : X; a.has_r = R != nullptr;
+  a.w = weight; a.b = bias ? bias : weight; a.has_b = bias != nullptr;
+  a.S = S; a.Y = Y; a.mean_out = mean; a.rstd_out = rstd;
+  return check_cuda(launch_norm_fwd(a, static_cast<cudaStream_t>(stream)), "qlora_layer_norm_fwd launch");
+}
+
+int qlora_layer_norm_workspace_size(const qlora_norm_t* n, int32_t with_dbias, size_t* bytes) {
+  if (!bytes) return fail(QLORA_ERR_INVALID_ARG, "bytes is NULL");
+  int rc = check_norm(n);
+  if (rc) return rc;
+  *bytes = norm_workspace_bytes(n->M, n->D, n->dtype, with_dbias != 0);
+  return ok();
+}
+
+int qlora_layer_norm_bwd(const qlora_norm_t* n, const void* dY, const void* S, const void* weight, const float* mean,
+                         const float* rstd, const void* dS, void* dX, float* dweight, float* dbias, void* workspace,
+                         size_t workspace_bytes, qlora_stream_t stream) {
+  int rc = check_norm(n);
+  if (rc) return rc;
+  const bool some = n->M > 0;
+  if ((rc = check_ptr16(dY, "dY", some)) || (rc = check_ptr16(S, "S", some)) ||
+      (rc = check_ptr16(weight, "weight", true)) || (rc = check_ptr4(mean, "mean", some && !n->rms)) ||
+      (rc = check_ptr4(rstd, "rstd", some)) || (rc = check_ptr16(dS, "dS", false)) ||
+      (rc = check_ptr16(dX, "dX", false)) || (rc = check_ptr16(dweight, "dweight", true)) ||
+      (rc = check_ptr16(dbias, "dbias", false)))
+    return rc;
+  if (dS && !dX && some) return fail(QLORA_ERR_INVALID_ARG, "dS without dX");
+  DeviceScope scope;
+  // sizes depend on the device's SM count: ask with the data's device current
+  if ((rc = scope.bind(dweight))) return rc;
+  const size_t need = norm_workspace_bytes(n->M, n->D, n->dtype, dbias != nullptr);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(QLORA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : 0);
+  if (workspace && (rc = check_ptr16(workspace, "workspace", false))) return rc;
+  NormArgs a = norm_args(n);
+  a.dY = dY; a.X = S; a.w = weight; a.mean_in = n->rms ? rstd : mean; a.rstd_in = rstd;
+  a.dS = dS ? dS : S; a.has_ds = dS != nullptr; a.dX = dX;
+  a.dw = dweight; a.db = dbias; a.part = static_cast<float*>(workspace);
+  return check_cuda(launch_norm_bwd(a, static_cast<cudaStream_t>(stream)), "qlora_layer_norm_bwd launch");
+}
+
 int qlora_nf4_codebook(float out[16]) {
   if (!out) return fail(QLORA_ERR_INVALID_ARG, "out is NULL");
   host_codebook(out);

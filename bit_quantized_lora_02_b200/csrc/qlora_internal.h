@@ -1,6 +1,7 @@
 // qlora_internal.h -- host-side declarations shared by the library's sources.
 #pragma once
 
+#include <algorithm>
 #include <cstddef>
 #include <cstdint>
 #include <map>
@@ -46,6 +47,30 @@ cudaError_t launch_dropout_bits(int64_t n, const DropoutArgs& d, uint32_t* bits,
 // dX (M x k, bf16, in place) += dscale * keep . (U A), U = U_s (M x rp), A (r x k)
 cudaError_t launch_lora_up_dropout(const uint16_t* U, int rp, const uint16_t* A, int r, const uint32_t* keep,
                                    float dscale, int64_t M, int64_t k, uint16_t* dX, cudaStream_t st);
+
+// layer norm (qlora_norm.cu)
+constexpr int64_t kNormMaxDim = 16384;
+struct NormArgs {
+  int64_t M;
+  int D;
+  int dtype, wdtype;        // QLORA_DT_* of the activations and of weight and bias
+  int rms;
+  float eps;
+  const void *X, *R;        // forward: input and residual; backward: X is the normalised S
+  const void *w, *b;
+  void *S, *Y;
+  float *mean_out, *rstd_out;
+  const void *dY, *dS;
+  const float *mean_in, *rstd_in;
+  void* dX;
+  float *dw, *db, *part;    // part: one row of partial sums per CTA
+  // Which optional inputs there are.  A pointer to one that is absent is set to
+  // another input of at least its size, so that no load has a wild address.
+  int has_r, has_b, has_ds;
+};
+size_t norm_workspace_bytes(int64_t M, int64_t D, int dtype, bool dbias);
+cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t st);
 
 // linear layer (qlora_gemm.cu)
 struct LinearArgs {

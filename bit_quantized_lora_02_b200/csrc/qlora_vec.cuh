@@ -1,0 +1,95 @@
+// qlora_vec.cuh -- 16-byte access to rows of bf16 or fp32 values, and the warp
+// reductions that the row kernels (layer norm, token log probabilities) share.
+//
+// Windows: a row that starts `sh` elements past a 16-byte boundary is covered
+// by aligned 16-byte windows; window c holds columns c * N - sh + i, i < N.
+// Only a row's first and last window can reach outside [0, cols); they are
+// read and written element by element, so nothing outside the row is touched.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "qlora_device.cuh"
+
+namespace qlora {
+
+template <typename T>
+struct Vec;
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
+    f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
+    f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+  }
+};
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// Columns col .. col + N - 1 of a row (col may be negative or reach past cols:
+// those elements become `fill`).  `p` is the row's first element; p + col is
+// 16-byte aligned.  The element loads clamp their column, so that their
+// addresses lie in the row whether or not the compiler keeps them behind the
+// comparison.
+template <typename T>
+__device__ __forceinline__ void load_window(const T* p, int col, int cols, float fill,
+                                            float (&f)[Vec<T>::N]) {
+  constexpr int N = Vec<T>::N;
+  if (col >= 0 && col + N <= cols) {
+    Vec<T>::unpack(*reinterpret_cast<const uint4*>(p + col), f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = fill;
+    if (col < cols && col > -N) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float x = to_f32(p[min(max(col + i, 0), cols - 1)]);
+        f[i] = (col + i >= 0 && col + i < cols) ? x : fill;
+      }
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_window(T* p, int col, int cols, const float (&f)[Vec<T>::N]) {
+  constexpr int N = Vec<T>::N;
+  if (col >= 0 && col + N <= cols) {
+    *reinterpret_cast<uint4*>(p + col) = Vec<T>::pack(f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (col + i >= 0 && col + i < cols) p[col + i] = from_f32<T>(f[i]);
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+}  // namespace qlora

@@ -311,6 +311,63 @@ int qlora_linear_bwd_dropout(const uint16_t *dY, const uint16_t *X, int64_t M, c
                              const qlora_dropout_t *drop, const uint16_t *T_save, uint16_t *dX, float *dA, float *dB,
                              void *workspace, size_t workspace_bytes, qlora_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The operators around the linear layer in a fine-tuning step.  The pages
+ * train the adapters inside a transformer ("LoRA and QLoRA: Efficient
+ * Fine-Tuning of Large Language Models" (fromzero2ai.dev), "Python
+ * Implementation: Fine-Tuning with PEFT and BitsAndBytes"); these entry points
+ * are what that step runs beside the projections.  They follow the
+ * conventions above, except that they leave the calling thread's current
+ * device as it was, and say themselves what they do with non-finite values.
+ * ------------------------------------------------------------------------ */
+
+/* Types of a tensor argument declared `void *`. */
+enum { QLORA_DT_BF16 = 0, QLORA_DT_F32 = 1 };
+
+/* Layer norm of M rows of D values (Ba, Kiros and Hinton, "Layer
+ * Normalization", 2016; rms: Zhang and Sennrich, "Root Mean Square Layer
+ * Normalization", 2019). */
+typedef struct {
+  int64_t M;       /* rows, >= 0                                             */
+  int64_t D;       /* values per row, 1 .. 16384                             */
+  int32_t dtype;   /* QLORA_DT_* of X, R, S, Y, dY, dS and dX                */
+  int32_t wdtype;  /* QLORA_DT_* of weight and bias                          */
+  int32_t rms;     /* 0: layer norm; 1: no mean is subtracted                */
+  float eps;       /* added to the variance (rms: to the mean square), >= 0  */
+} qlora_norm_t;
+
+/* Forward, with the residual add that precedes the norm in a transformer:
+ *     S = X + R  (rounded to the activations' type; S = X without R),
+ *     mean = sum(S) / D  (rms: 0),  rstd = 1 / sqrt(sum((S - mean)^2) / D + eps),
+ *     Y = (S - mean) rstd weight + bias.
+ *   X, R, S, Y : M x D.  R may be NULL; S is written when R is given and must
+ *                be NULL otherwise.  Y and S may be X's or R's memory.
+ *   weight     : D values.   bias : D values or NULL.
+ *   mean, rstd : M fp32 each for qlora_layer_norm_bwd; either may be NULL (mean
+ *                is written as 0 for rms).
+ * Sums are fp32; each output is rounded once.  A row with a non-finite value
+ * gives NaN in that row's Y and nowhere else. */
+int qlora_layer_norm_fwd(const qlora_norm_t *n, const void *X, const void *R, const void *weight, const void *bias,
+                         void *S, void *Y, float *mean, float *rstd, qlora_stream_t stream);
+
+/* Workspace bytes of qlora_layer_norm_bwd (with_dbias: whether dbias is
+ * wanted).  Host-only. */
+int qlora_layer_norm_workspace_size(const qlora_norm_t *n, int32_t with_dbias, size_t *bytes);
+
+/* Backward: with xh = (S - mean) rstd and g = dY weight,
+ *     dX = rstd (g - sum(g) / D - xh sum(g xh) / D) + dS   (rms: no sum(g) / D),
+ *     dweight = sum over rows of dY xh,   dbias = sum over rows of dY.
+ *   S          : the normalised input (the forward's S, or its X without R).
+ *   mean, rstd : as the forward wrote them (mean may be NULL for rms).
+ *   dS         : M x D gradient that reaches S along the residual stream, or NULL.
+ *   dX         : M x D, the gradient of X and of R alike; NULL skips it.  It
+ *                may be dY's or dS's memory.
+ *   dweight, dbias : D fp32, written, not accumulated; dbias may be NULL.
+ * Deterministic.  M == 0 writes zeros to dweight and dbias. */
+int qlora_layer_norm_bwd(const qlora_norm_t *n, const void *dY, const void *S, const void *weight, const float *mean,
+                         const float *rstd, const void *dS, void *dX, float *dweight, float *dbias, void *workspace,
+                         size_t workspace_bytes, qlora_stream_t stream);
+
 /* The library's NF4 table C[0..15] (fp32, ascending) copied to host memory. */
 int qlora_nf4_codebook(float out[16]);
 
@@ -339,7 +396,8 @@ enum {
   QLORA_KC_FWD_GEMM = 3,   /* fused dequant + LoRA forward GEMM                */
   QLORA_KC_BWD_GEMM = 4,   /* fused dequant + LoRA backward (dX) GEMM          */
   QLORA_KC_LORA_GEMM = 5,  /* low-rank GEMMs: s X A^T, s dY B, dA, dB          */
-  QLORA_KC_AUX = 6,        /* split-K reductions, transposes                   */
+  QLORA_KC_AUX = 6,        /* split-K reductions, transposes; the operators around
+                            * the linear layer                                 */
   QLORA_KC_COUNT = 7
 };
 

@@ -1,0 +1,225 @@
+"""Layer norm (forward with the residual add, backward with the weight's
+gradient) against a plain 64-bit form.
+
+Tolerances.  u = 2^-24 is half a step of fp32.  A row's sums take fewer than 64
+additions on any path from a value to the total (at most 32 values per thread,
+5 shuffles, 17 warps), so a sum is off by at most 64 u times the sum of
+magnitudes; the few products behind it and the square root add less than that
+again: 128 u times the magnitudes that enter.  The weight's gradient adds M
+rows: (M + 16) u.  An output in bf16 adds half a step, 2^-8 of its value."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import step_oracle as SO
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import bit_quantized_lora_02_b200 as Q
+
+U = 2.0 ** -24
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def half(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def f64(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def inputs(M, D, dtype, wdtype, seed, bias, residual):
+    g = torch.Generator().manual_seed(seed)
+    X = (torch.randn(M, D, generator=g) * 2 + 0.5).to(dtype).cuda()
+    R = torch.randn(M, D, generator=g).to(dtype).cuda() if residual else None
+    w = (1 + 0.2 * torch.randn(D, generator=g)).to(wdtype).cuda()
+    b = torch.randn(D, generator=g).to(wdtype).cuda() if bias else None
+    dY = torch.randn(M, D, generator=g).to(dtype).cuda()
+    dS = torch.randn(M, D, generator=g).to(dtype).cuda() if residual else None
+    return X, R, w, b, dY, dS
+
+
+def check_forward(X, R, w, b, eps, rms, Y, S, mean, rstd):
+    ref_S = X if R is None else (X.float() + R.float()).to(X.dtype)
+    assert torch.equal(S, ref_S)
+    x = f64(S)
+    Yr, mr, rr = SO.norm_forward(x, f64(w), f64(b), eps, rms)
+    size = np.abs(x).mean(axis=1)
+    if not rms:
+        assert np.all(np.abs(f64(mean) - mr) <= 128 * U * size + 1e-40)
+    # the variance is off by 128 u of itself and by what the mean's error adds
+    assert np.all(np.abs(f64(rstd) / rr - 1) <= 128 * U * (1 + (0 if rms else 1) * size * rr))
+    term = np.abs(f64(w)) * rr[:, None] * (np.abs(x) + size[:, None]) * (1 + size * rr)[:, None]
+    tol = 128 * U * (term + (0 if b is None else np.abs(f64(b)))) + half(X.dtype) * np.abs(Yr) * 1.01 + 1e-40
+    assert np.all(np.abs(f64(Y) - Yr) <= tol)
+
+
+def check_backward(dY, S, w, mean, rstd, dS, rms, dX, dw, db):
+    r = SO.norm_backward(f64(dY), f64(S), f64(w), f64(mean), f64(rstd), f64(dS), rms)
+    M = S.shape[0]
+    g = np.abs(f64(dY) * f64(w))
+    xs = f64(S)
+    centre = 0.0 if rms else f64(mean)[:, None]
+    rs = f64(rstd)[:, None]
+    xh = (np.abs(xs) + np.abs(centre)) * rs           # bounds |xh| and its rounding
+    term = rs * (g + g.mean(1, keepdims=True) + xh * (g * xh).mean(1, keepdims=True))
+    tol = 128 * U * (term + (0 if dS is None else np.abs(f64(dS)))) + half(S.dtype) * np.abs(r[0]) * 1.01 + 1e-40
+    assert np.all(np.abs(f64(dX) - r[0]) <= tol)
+    rows = (M + 16) * U
+    assert np.all(np.abs(f64(dw) - r[1]) <= rows * (np.abs(f64(dY)) * xh).sum(0) + 1e-40)
+    if db is not None:
+        assert np.all(np.abs(f64(db) - r[2]) <= rows * np.abs(f64(dY)).sum(0) + 1e-40)
+
+
+CASES = [(M, D) for M, D in ((1, 1), (2, 7), (5, 64), (3, 255), (9, 256), (700, 257), (4, 512), (33, 1000), (5, 1024),
+                             (700, 1025), (2, 2047), (150, 2048), (303, 2049), (7, 4096), (310, 4099), (151, 5003),
+                             (1, 8192), (160, 8192), (300, 8191), (160, 8193), (1, 16384), (150, 16384), (301, 16381),
+                             (2000, 300), (1300, 511))]
+
+
+@pytest.mark.parametrize("M,D", CASES)
+@pytest.mark.parametrize("dtype,wdtype,rms,bias,residual", [
+    (BF16, F32, True, False, True), (BF16, BF16, False, True, False), (F32, F32, False, True, True),
+    (F32, BF16, True, True, False), (BF16, F32, False, False, True)] if torch.cuda.is_available() else [])
+def test_forward_and_backward(M, D, dtype, wdtype, rms, bias, residual):
+    X, R, w, b, dY, dS = inputs(M, D, dtype, wdtype, M + D, bias, residual)
+    Y, S, mean, rstd = Q.qlora_layer_norm_fwd(X, w, bias=b, residual=R, eps=1e-5, rms=rms)
+    assert (S is X) == (R is None) and (mean is None) == rms
+    check_forward(X, R, w, b, 1e-5, rms, Y, S, mean, rstd)
+    dX, dw, db = Q.qlora_layer_norm_bwd(dY, S, w, mean, rstd, dS=dS, rms=rms, need_dbias=bias)
+    assert (db is None) == (not bias)
+    check_backward(dY, S, w, mean, rstd, dS, rms, dX, dw, db)
+    again = Q.qlora_layer_norm_bwd(dY, S, w, mean, rstd, dS=dS, rms=rms, need_dbias=bias)
+    for p, q in zip((dX, dw, db), again):
+        assert p is None or torch.equal(p, q)                      # deterministic
+
+
+def test_every_width_class_with_one_row_and_many():
+    """Each width around the limits of the kernels' variants, with rows that start
+    at every offset from a 16-byte boundary."""
+    for D in (8, 9, 249, 250, 505, 506, 1017, 1018, 2041, 2042, 4089, 4090, 8185, 8186, 16377, 16378):
+        for M in (1, 17):
+            X, R, w, b, dY, dS = inputs(M, D, BF16, F32, D, True, True)
+            Y, S, mean, rstd = Q.qlora_layer_norm_fwd(X, w, bias=b, residual=R)
+            check_forward(X, R, w, b, 1e-5, False, Y, S, mean, rstd)
+            dX, dw, db = Q.qlora_layer_norm_bwd(dY, S, w, mean, rstd, dS=dS, need_dbias=True)
+            check_backward(dY, S, w, mean, rstd, dS, False, dX, dw, db)
+
+
+def test_no_rows():
+    X = torch.empty(0, 96, dtype=BF16, device="cuda")
+    w = torch.ones(96, device="cuda")
+    Y, S, mean, rstd = Q.qlora_layer_norm_fwd(X, w)
+    assert Y.shape == (0, 96) and rstd.shape == (0,)
+    dX, dw, db = Q.qlora_layer_norm_bwd(X, X, w, mean, rstd, need_dbias=True,
+                                        dweight=torch.full((96,), 7.0, device="cuda"))
+    assert dX.shape == (0, 96) and not dw.any() and not db.any()
+
+
+@pytest.mark.parametrize("D", [1000, 1001, 8192, 8193])
+def test_nothing_is_written_outside_the_rows(D):
+    """Outputs are slices of larger buffers: the values around them stay."""
+    M = 5
+    X, R, w, b, dY, dS = inputs(M, D, BF16, F32, 3, True, True)
+
+    def framed():
+        buf = torch.full((M * D + 128,), 5.0, dtype=BF16, device="cuda")
+        return buf, buf[64:64 + M * D].view(M, D)
+    (by, Y), (bs, S), (bx, dX) = framed(), framed(), framed()
+    _, _, mean, rstd = Q.qlora_layer_norm_fwd(X, w, bias=b, residual=R, Y=Y, S=S)
+    Q.qlora_layer_norm_bwd(dY, S, w, mean, rstd, dS=dS, dX=dX)
+    for buf in (by, bs, bx):
+        assert (buf[:64] == 5).all() and (buf[64 + M * D:] == 5).all()
+
+
+@pytest.mark.parametrize("D", [4096, 4097])
+def test_in_place(D):
+    M = 200
+    X, R, w, b, dY, dS = inputs(M, D, BF16, F32, 11, True, True)
+    Y, S, mean, rstd = Q.qlora_layer_norm_fwd(X, w, bias=b, residual=R)
+    x, r = X.clone(), R.clone()
+    Y2, S2, m2, r2 = Q.qlora_layer_norm_fwd(x, w, bias=b, residual=r, Y=x, S=r)
+    assert torch.equal(Y, Y2) and torch.equal(S, S2) and torch.equal(mean, m2) and torch.equal(rstd, r2)
+    dX, dw, db = Q.qlora_layer_norm_bwd(dY, S, w, mean, rstd, dS=dS, need_dbias=True)
+    for name in ("dY", "dS"):
+        a, c = dY.clone(), dS.clone()
+        got = Q.qlora_layer_norm_bwd(a, S, w, mean, rstd, dS=c, need_dbias=True, dX=a if name == "dY" else c)
+        assert torch.equal(got[0], dX) and torch.equal(got[1], dw) and torch.equal(got[2], db)
+
+
+def test_large_mean_and_tiny_variance():
+    """The variance is summed around the mean, so a common offset costs nothing
+    but the offset's own rounding; a constant row is divided by sqrt(eps)."""
+    D = 4096
+    g = torch.Generator().manual_seed(0)
+    X = (torch.randn(64, D, generator=g) + 1000.0).cuda()
+    X[3] = 2.5
+    w = torch.ones(D, device="cuda")
+    Y, S, mean, rstd = Q.qlora_layer_norm_fwd(X, w, eps=1e-5)
+    check_forward(X, None, w, None, 1e-5, False, Y, S, mean, rstd)
+    assert not Y[3].any()
+    Y, _, _, rstd = Q.qlora_layer_norm_fwd(torch.zeros(2, D, device="cuda"), w, eps=1e-5, rms=True)
+    assert not Y.any() and torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5))
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_non_finite_value_stays_in_its_row(value):
+    X, _, w, b, _, _ = inputs(300, 1001, BF16, F32, 5, True, False)
+    clean, _, _, _ = Q.qlora_layer_norm_fwd(X, w, bias=b)
+    X[17, 400] = value
+    Y, _, _, _ = Q.qlora_layer_norm_fwd(X, w, bias=b)
+    keep = torch.arange(300, device="cuda") != 17
+    assert Y[17].isnan().all() and torch.equal(Y[keep], clean[keep])
+
+
+def test_gradient_against_differences():
+    """Central differences of a weighted sum of the forward's outputs, in fp32:
+    step h = 2^-4, so the difference is off by at most 2 * 128 u |f| / (2 h) for
+    rounding and by h^2 / 6 of the third derivative, which for values of order
+    one over D = 40 entries stays below 0.02 here."""
+    D, h = 40, 2.0 ** -4
+    X, R, w, b, dY, dS = inputs(3, D, F32, F32, 1, True, True)
+
+    def f(X_, w_, b_):
+        Y, S, _, _ = Q.qlora_layer_norm_fwd(X_, w_, bias=b_, residual=R)
+        return ((Y.double() * dY.double()).sum() + (S.double() * dS.double()).sum()).item()
+    _, S, mean, rstd = Q.qlora_layer_norm_fwd(X, w, bias=b, residual=R)
+    dX, dw, db = Q.qlora_layer_norm_bwd(dY, S, w, mean, rstd, dS=dS, need_dbias=True)
+    for i, j in ((0, 0), (1, 17), (2, 39)):
+        for t, grad in ((X, dX[i, j]), (w, dw[j]), (b, db[j])):
+            at = (i, j) if t is X else (j,)
+            up, down = t.clone(), t.clone()
+            up[at] += h
+            down[at] -= h
+            args = [(up if t is x else x, down if t is x else x) for x in (X, w, b)]
+            num = (f(*(p for p, _ in args)) - f(*(q for _, q in args))) / (2 * h)
+            assert abs(num - grad.item()) <= 0.02
+
+
+def test_captured_and_replayed_on_a_side_stream():
+    M, D = 300, 4099
+    X, R, w, b, dY, dS = inputs(M, D, BF16, F32, 2, True, True)
+    want_f = Q.qlora_layer_norm_fwd(X, w, bias=b, residual=R)
+    want_b = Q.qlora_layer_norm_bwd(dY, want_f[1], w, want_f[2], want_f[3], dS=dS, need_dbias=True)
+    other = X.clone() * 2
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    buf = other.clone()
+    with torch.cuda.graph(graph):
+        f = Q.qlora_layer_norm_fwd(buf, w, bias=b, residual=R)
+        g = Q.qlora_layer_norm_bwd(dY, f[1], w, f[2], f[3], dS=dS, need_dbias=True)
+    graph.replay()
+    buf.copy_(X)
+    graph.replay()
+    torch.cuda.synchronize()
+    for p, q in zip(want_f + want_b, f + g):
+        assert torch.equal(p, q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    f = Q.qlora_layer_norm_fwd(X, w, bias=b, residual=R, stream=side)
+    g = Q.qlora_layer_norm_bwd(dY, f[1], w, f[2], f[3], dS=dS, need_dbias=True, stream=side)
+    side.synchronize()
+    for p, q in zip(want_f + want_b, f + g):
+        assert torch.equal(p, q)
