@@ -601,15 +601,32 @@ def _on_cuda(t: torch.Tensor, name: str) -> torch.device:
     return t.device
 
 
+_NO_CONTEXT = contextlib.nullcontext()
+# the raw handle of a device's current stream, without building a Stream object where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _enter(dev: torch.device, stream):
     """(raw stream, context for the call's own allocations): the current stream
     of the tensors' device, or the caller's stream, which then also owns what
     the call allocates."""
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream, contextlib.nullcontext()
+        return _raw_stream(dev.index), _NO_CONTEXT
     if stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, the call runs on {dev}")
     return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def _want(t: Optional[torch.Tensor], name: str, shape, dtype, dev: torch.device) -> Optional[int]:
+    """The address of an argument that must have this shape and dtype, be
+    contiguous and live on ``dev``; None for an absent one."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _expect(t, name, shape, dtype)
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the call runs on {dev}")
+    return t.data_ptr()
 
 
 def _norm_struct(X: torch.Tensor, weight: torch.Tensor, name: str, rms: bool, eps: float) -> QloraNorm:
@@ -627,40 +644,50 @@ def qlora_layer_norm_fwd(X: torch.Tensor, weight: torch.Tensor, bias: Optional[t
     (Y, S, mean, rstd) for qlora_layer_norm_bwd; S is X without a residual and
     mean is None for rms.  Y and S may be X or residual (in place)."""
     n = _norm_struct(X, weight, "X", rms, eps)
-    M, D = X.shape
-    _expect(X, "X", (M, D), X.dtype)
-    _expect(residual, "residual", (M, D), X.dtype, required=False)
-    _expect(weight, "weight", (D,), weight.dtype)
-    _expect(bias, "bias", (D,), weight.dtype, required=False)
+    shape, dtype, dev, f32 = X.shape, X.dtype, X.device, torch.float32
+    M, D = shape
     if S is not None and residual is None:
         raise ValueError("S goes with residual")
     if mean is not None and rms:
         raise ValueError("mean is not used with rms")
-    for t, name, shape, dtype in ((Y, "Y", (M, D), X.dtype), (S, "S", (M, D), X.dtype),
-                                  (mean, "mean", (M,), torch.float32), (rstd, "rstd", (M,), torch.float32)):
-        _expect(t, name, shape, dtype, required=False)
-    dev = _on_cuda(X, "X")
-    _same_device(dev, residual=residual, weight=weight, bias=bias, Y=Y, S=S, mean=mean, rstd=rstd)
+    pX = _want(X, "X", shape, dtype, dev)
+    pR = _want(residual, "residual", shape, dtype, dev)
+    pw = _want(weight, "weight", (D,), weight.dtype, dev)
+    pb = _want(bias, "bias", (D,), weight.dtype, dev)
+    pY, pS = _want(Y, "Y", shape, dtype, dev), _want(S, "S", shape, dtype, dev)
+    pm, pr = _want(mean, "mean", (M,), f32, dev), _want(rstd, "rstd", (M,), f32, dev)
+    _on_cuda(X, "X")
     raw, own = _enter(dev, stream)
     with own:
         if Y is None:
             Y = torch.empty_like(X)
+            pY = Y.data_ptr()
         if S is None and residual is not None:
             S = torch.empty_like(X)
+            pS = S.data_ptr()
         if mean is None and not rms:
-            mean = torch.empty(M, dtype=torch.float32, device=dev)
+            mean = torch.empty(M, dtype=f32, device=dev)
+            pm = mean.data_ptr()
         if rstd is None:
-            rstd = torch.empty(M, dtype=torch.float32, device=dev)
-    _check(lib().qlora_layer_norm_fwd(ctypes.byref(n), X.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias),
-                                      _ptr(S), Y.data_ptr(), _ptr(mean), rstd.data_ptr(), raw))
+            rstd = torch.empty(M, dtype=f32, device=dev)
+            pr = rstd.data_ptr()
+    _check(lib().qlora_layer_norm_fwd(ctypes.byref(n), pX, pR, pw, pb, pS, pY, pm, pr, raw))
     return Y, (X if S is None else S), mean, rstd
 
 
+def _norm_workspace(n: QloraNorm, with_dbias: bool, dev: Optional[torch.device] = None) -> int:
+    size = ctypes.c_size_t()
+    # the size goes by the SM count of the current device
+    with contextlib.nullcontext() if dev is None or dev.index == torch.cuda.current_device() else torch.cuda.device(dev):
+        _check(lib().qlora_layer_norm_workspace_size(ctypes.byref(n), int(with_dbias), ctypes.byref(size)))
+    return size.value
+
+
 def qlora_layer_norm_workspace_size(M: int, D: int, dtype=torch.bfloat16, with_dbias: bool = False) -> int:
-    n = ctypes.c_size_t()
-    st = QloraNorm(M, D, _DT[dtype], 1, 0, 0.0)
-    _check(lib().qlora_layer_norm_workspace_size(ctypes.byref(st), int(with_dbias), ctypes.byref(n)))
-    return n.value
+    """Bytes of the backward pass's workspace on the current device."""
+    if dtype not in _DT:
+        raise ValueError(f"dtype {dtype}, expected torch.bfloat16 or torch.float32")
+    return _norm_workspace(QloraNorm(M, D, _DT[dtype], 1, 0, 0.0), with_dbias)
 
 
 def qlora_layer_norm_bwd(dY: torch.Tensor, S: torch.Tensor, weight: torch.Tensor, mean: Optional[torch.Tensor],
@@ -673,34 +700,33 @@ def qlora_layer_norm_bwd(dY: torch.Tensor, S: torch.Tensor, weight: torch.Tensor
     reaches S along the residual stream.  dweight and dbias are fp32; dbias is
     computed with need_dbias or where a tensor for it is given."""
     n = _norm_struct(S, weight, "S", rms, 0.0)
-    M, D = S.shape
-    f32 = torch.float32
-    _expect(S, "S", (M, D), S.dtype)
-    _expect(dY, "dY", (M, D), S.dtype)
-    _expect(weight, "weight", (D,), weight.dtype)
-    _expect(mean, "mean", (M,), f32, required=not rms)
-    _expect(rstd, "rstd", (M,), f32)
-    for t, name, shape, dtype in ((dS, "dS", (M, D), S.dtype), (dX, "dX", (M, D), S.dtype),
-                                  (dweight, "dweight", (D,), f32), (dbias, "dbias", (D,), f32)):
-        _expect(t, name, shape, dtype, required=False)
-    dev = _on_cuda(S, "S")
-    _same_device(dev, dY=dY, weight=weight, mean=mean, rstd=rstd, dS=dS, dX=dX, dweight=dweight, dbias=dbias,
-                 workspace=workspace)
+    shape, dtype, dev, f32 = S.shape, S.dtype, S.device, torch.float32
+    M, D = shape
+    if rstd is None or (mean is None and not rms):
+        raise ValueError("mean is required" if rstd is not None else "rstd is required")
+    pdY, pS = _want(dY, "dY", shape, dtype, dev), _want(S, "S", shape, dtype, dev)
+    pw = _want(weight, "weight", (D,), weight.dtype, dev)
+    pm, pr = None if rms else _want(mean, "mean", (M,), f32, dev), _want(rstd, "rstd", (M,), f32, dev)
+    pdS, pdX = _want(dS, "dS", shape, dtype, dev), _want(dX, "dX", shape, dtype, dev)
+    pdw, pdb = _want(dweight, "dweight", (D,), f32, dev), _want(dbias, "dbias", (D,), f32, dev)
+    _on_cuda(S, "S")
+    if workspace is not None:
+        _same_device(dev, workspace=workspace)
     raw, own = _enter(dev, stream)
     with own:
         if dX is None:
             dX = torch.empty_like(S)
+            pdX = dX.data_ptr()
         if dweight is None:
             dweight = torch.empty(D, dtype=f32, device=dev)
+            pdw = dweight.data_ptr()
         if dbias is None and need_dbias:
             dbias = torch.empty(D, dtype=f32, device=dev)
+            pdb = dbias.data_ptr()
         if workspace is None:
-            with torch.cuda.device(dev):
-                nws = qlora_layer_norm_workspace_size(M, D, S.dtype, dbias is not None)
-            workspace = torch.empty(max(nws, 16), dtype=torch.uint8, device=dev)
-    _check(lib().qlora_layer_norm_bwd(ctypes.byref(n), dY.data_ptr(), S.data_ptr(), weight.data_ptr(),
-                                      None if rms else mean.data_ptr(), rstd.data_ptr(), _ptr(dS), dX.data_ptr(),
-                                      dweight.data_ptr(), _ptr(dbias), workspace.data_ptr(), _nbytes(workspace), raw))
+            workspace = torch.empty(max(_norm_workspace(n, dbias is not None, dev), 16), dtype=torch.uint8, device=dev)
+    _check(lib().qlora_layer_norm_bwd(ctypes.byref(n), pdY, pS, pw, pm, pr, pdS, pdX, pdw, pdb, workspace.data_ptr(),
+                                      _nbytes(workspace), raw))
     return dX, dweight, dbias
 
 

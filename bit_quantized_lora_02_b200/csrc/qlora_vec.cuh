@@ -50,40 +50,64 @@ __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-// Columns col .. col + N - 1 of a row (col may be negative or reach past cols:
-// those elements become `fill`).  `p` is the row's first element; p + col is
-// 16-byte aligned.  The element loads clamp their column, so that their
-// addresses lie in the row whether or not the compiler keeps them behind the
-// comparison.
-template <typename T>
-__device__ __forceinline__ void load_window(const T* p, int col, int cols, float fill,
-                                            float (&f)[Vec<T>::N]) {
+// Columns col .. col + N - 1 of a row, packed (col may be negative or reach past
+// cols: those elements become zero).  `p` is the row's first element; p + col
+// is 16-byte aligned.  WHOLE: a window lies in the row or past it, never across
+// an end.  The element loads clamp their column, so that their addresses lie in
+// the row whether or not the compiler keeps them behind the comparison.
+template <typename T, bool WHOLE>
+__device__ __forceinline__ uint4 load_raw(const T* p, int col, int cols) {
   constexpr int N = Vec<T>::N;
-  if (col >= 0 && col + N <= cols) {
-    Vec<T>::unpack(*reinterpret_cast<const uint4*>(p + col), f);
-  } else {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (WHOLE ? col < cols : (col >= 0 && col + N <= cols)) {
+    v = *reinterpret_cast<const uint4*>(p + col);
+  } else if (!WHOLE && col < cols && col > -N) {
+    float f[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = fill;
-    if (col < cols && col > -N) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float x = to_f32(p[min(max(col + i, 0), cols - 1)]);
-        f[i] = (col + i >= 0 && col + i < cols) ? x : fill;
-      }
+    for (int i = 0; i < N; ++i) {
+      const float x = to_f32(p[min(max(col + i, 0), cols - 1)]);
+      f[i] = (col + i >= 0 && col + i < cols) ? x : 0.0f;
     }
+    v = Vec<T>::pack(f);
   }
+  return v;
 }
 
-template <typename T>
-__device__ __forceinline__ void store_window(T* p, int col, int cols, const float (&f)[Vec<T>::N]) {
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void store_raw(T* p, int col, int cols, const uint4& v) {
   constexpr int N = Vec<T>::N;
-  if (col >= 0 && col + N <= cols) {
-    *reinterpret_cast<uint4*>(p + col) = Vec<T>::pack(f);
-  } else {
+  if (WHOLE ? col < cols : (col >= 0 && col + N <= cols)) {
+    *reinterpret_cast<uint4*>(p + col) = v;
+  } else if (!WHOLE) {
+    float f[N];
+    Vec<T>::unpack(v, f);
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (col + i >= 0 && col + i < cols) p[col + i] = from_f32<T>(f[i]);
   }
+}
+
+// 16 bytes from global to shared memory without passing through registers; only
+// the first `bytes` are read, the rest of the 16 become zero.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Wait until at most `left` of this thread's latest groups are in flight (0..3).
+__device__ __forceinline__ void cp_async_wait(int left) {
+  if (left >= 3)
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (left == 2)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (left == 1)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
