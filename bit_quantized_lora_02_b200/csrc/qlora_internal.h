@@ -67,7 +67,8 @@ struct NormArgs {
   // Which optional inputs there are.  A pointer to one that is absent is set to
   // another input of at least its size, so that no load has a wild address.
   int has_r, has_b, has_ds;
-  int stages;               // backward: rows that the loads run ahead
+  int stages;               // rows that the loads run ahead
+  int ring_ds;              // backward: dS passes through the ring as well
 };
 size_t norm_workspace_bytes(int64_t M, int64_t D, int dtype, bool dbias);
 cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t st);

@@ -21,28 +21,119 @@ namespace qlora {
 
 namespace {
 
-// A reduction over the CTA's threads: one barrier each.  The caller alternates
-// `buf` between two halves of the scratch, so a fast warp's next partial sums
-// cannot meet a slow warp's reads.  Every thread adds the warps' sums in the
-// same order.
-template <int NT>
-__device__ __forceinline__ float cta_sum(float v, float* scratch, int buf) {
-  v = warp_sum(v);
-  if constexpr (NT == 32) return v;
-  constexpr int NW = NT / 32;
-  float* s = scratch + buf * 32;
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float t = 0.0f;
+// Both kernels walk over rows gridDim apart.  A row is held by a CTA, or by one
+// of its four warps where it is short (WARP), CH windows of 16 bytes to a thread.
+// The CTA has as many warps as the row needs at CH windows each.  A thread has the same columns in every row: the weight stays in
+// registers, and the backward pass sums its gradient there.  Rows that do not
+// start on 16-byte boundaries shift the windows; the grid is then a multiple of
+// the 8 (fp32: 4) rows after which the shift repeats, so that the columns still
+// never change.
+//
+// The rows' loads run ahead through a ring of a.stages rows in shared memory
+// (cp.async): what is in flight then depends neither on registers nor on how
+// many CTAs are resident.  Each thread reads back only the 16-byte slots that it
+// filled itself, so the ring needs no barrier; the barriers belong to the rows'
+// sums.  32 values per thread, where the row is long enough: the shuffles,
+// barriers and addresses of a row cost as much as 10 values' arithmetic.
+template <typename T, bool WARP, int CH, bool ALIGNED>
+struct Rows {
+  static constexpr int N = Vec<T>::N;
+  static constexpr int ROWS = WARP ? 4 : 1;
+  int t, r, sh, D;
+  int nt, tb;          // threads of the row, of the CTA
+  int64_t row0, stride, M;
+  uint32_t slot0, stage_bytes;
+
+  __device__ __forceinline__ Rows(int64_t M_, int D_, void* ring, int arrays) : D(D_), M(M_) {
+    tb = WARP ? 128 : blockDim.x;
+    nt = WARP ? 32 : blockDim.x;
+    t = WARP ? (threadIdx.x & 31) : threadIdx.x;
+    r = WARP ? (threadIdx.x >> 5) : 0;
+    row0 = static_cast<int64_t>(blockIdx.x) * ROWS + r;
+    stride = static_cast<int64_t>(gridDim.x) * ROWS;
+    sh = ALIGNED ? 0 : static_cast<int>((row0 * D) % N);
+    slot0 = smem_u32(ring) + threadIdx.x * 16u;
+    stage_bytes = static_cast<uint32_t>(arrays * CH * tb * 16);
+  }
+  // what window c can read: 16 bytes, fewer at the row's end, none past it
+  __device__ __forceinline__ int bytes(int c) const {
+    if constexpr (ALIGNED) return col(c) < D ? 16 : 0;
+    return min(max(D - col(c), 0), N) * static_cast<int>(sizeof(T));
+  }
+  __device__ __forceinline__ int col(int c) const { return (t + c * nt) * N - sh; }
+  // Start the loads of array k of a row (element offset `at`) into a stage.  A
+  // window that starts in the row before reads that row's end too.
+  __device__ __forceinline__ void copy(const void* base, int64_t at, int k, uint32_t stage) const {
+    const T* p = reinterpret_cast<const T*>(base) + at - sh;
+    uint32_t dst = slot0 + stage + static_cast<uint32_t>(k * CH * tb * 16);
 #pragma unroll
-  for (int w = 0; w < NW; ++w) t += s[w];
-  return t;
+    for (int c = 0; c < CH; ++c, dst += tb * 16) {
+      const int n = bytes(c);
+      cp_async16(dst, p + (n ? (t + c * nt) * N : 0), n);
+    }
+  }
+  __device__ __forceinline__ uint4 get(int k, int c, uint32_t stage) const {
+    return lds128(slot0 + stage + static_cast<uint32_t>((k * CH + c) * tb * 16));
+  }
+  __device__ __forceinline__ void put(int k, int c, uint32_t stage, const uint4& v) const {
+    sts128(slot0 + stage + static_cast<uint32_t>((k * CH + c) * tb * 16), v);
+  }
+  // whether element i of window c belongs to the row
+  __device__ __forceinline__ bool in(int c, int i) const {
+    return ALIGNED ? col(c) < D : (col(c) + i >= 0 && col(c) + i < D);
+  }
+};
+
+// Sums of one or two values over the row's threads: one barrier.  The caller
+// alternates between two scratches, so a fast warp's next partial sums cannot
+// meet a slow warp's reads.  Slots of warps that the CTA does not have stay zero
+// (MAXW is the most it can have); every thread adds the slots in the same order.
+template <bool WARP, int MAXW>
+__device__ __forceinline__ f2 row_sum2(float a, float b, float4* scratch) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  f2 v = f2_make(a, b);
+  if constexpr (!WARP) {
+    if ((threadIdx.x & 31) == 0) reinterpret_cast<float2*>(scratch)[threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int w = 0; w < MAXW / 2; ++w) {
+      const float4 q = scratch[w];
+      v = f2_add(f2_add(v, f2_make(q.x, q.y)), f2_make(q.z, q.w));
+    }
+  }
+  return v;
 }
+template <bool WARP, int MAXW>
+__device__ __forceinline__ float row_sum(float a, float4* scratch) {
+  a = warp_sum(a);
+  if constexpr (!WARP) {
+    if ((threadIdx.x & 31) == 0) reinterpret_cast<float*>(scratch)[threadIdx.x >> 5] = a;
+    __syncthreads();
+    f2 v = 0, u = 0;
+#pragma unroll
+    for (int w = 0; w < MAXW / 4; ++w) {
+      const float4 q = scratch[w];
+      v = f2_add(v, f2_make(q.x, q.y));
+      u = f2_add(u, f2_make(q.z, q.w));
+    }
+    a = f2_sum(f2_add(v, u));
+  }
+  return a;
+}
+
+// CTAs of nt threads per SM at 128 registers per thread.
+constexpr int norm_ctas(int nt) { return nt <= 512 ? 512 / nt : 1; }
 
 // Columns col .. col + N - 1 of the weight or bias (bf16 or fp32, the same for
 // all threads; base 16-byte aligned).  Zero outside [0, D).
 template <int N>
-__device__ __forceinline__ void load_w(const void* w, bool bf16, int col, int D, float (&f)[N]) {
+__device__ __forceinline__ void load_w(const void* w, bool bf16, int col, int D, f2 (&out)[N / 2]) {
+  float f[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) f[i] = 0.0f;
   if (col >= 0 && col + N <= D && (col & 3) == 0) {
@@ -69,319 +160,297 @@ __device__ __forceinline__ void load_w(const void* w, bool bf16, int col, int D,
       f[i] = (col + i >= 0 && col + i < D) ? x : 0.0f;
     }
   }
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) out[i] = f2_make(f[2 * i], f[2 * i + 1]);
 }
 
 // ---------------------------------------------------------------------------
-// Forward.  NT threads hold one row, CH windows each; a warp holds a row of up
-// to 1024 values by itself (4 rows per CTA).  ALIGNED: every row starts on a
-// 16-byte boundary and ends on one, so no element needs a bounds check.
+// Forward.
 // ---------------------------------------------------------------------------
-// Rows in flight hide the loads: registers are held to what lets about 96 KB of
-// loads be outstanding on an SM.
-constexpr int fwd_ctas(int nt, int e) { return nt == 32 ? (e > 16 ? 5 : 8) : nt * e <= 2048 ? 8 : nt * e <= 4096 ? 4 : nt * e <= 8192 ? (nt > 512 ? 1 : 3) : 1; }
-
-template <typename T, int NT, int CH, bool ALIGNED>
-__global__ void __launch_bounds__(NT == 32 ? 128 : NT, fwd_ctas(NT, CH * Vec<T>::N)) k_norm_fwd(NormArgs a) {
-  constexpr int N = Vec<T>::N;
-  constexpr int ROWS = NT == 32 ? 4 : 1;
-  __shared__ float scratch[64];
-  const int t = NT == 32 ? (threadIdx.x & 31) : threadIdx.x;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * ROWS + (NT == 32 ? (threadIdx.x >> 5) : 0);
+template <typename T, int MAXT, int CH, bool ALIGNED>
+__global__ void __launch_bounds__(MAXT, norm_ctas(MAXT)) k_norm_fwd(NormArgs a) {
+  constexpr int H = Vec<T>::N / 2, MAXW = MAXT / 32;
+  constexpr bool WARP = MAXT == 128;
+  __shared__ float4 scratch[2][MAXW / 4];
+  extern __shared__ __align__(16) uint8_t ring[];
+  if constexpr (!WARP) {
+    for (int i = threadIdx.x; i < 2 * MAXW; i += blockDim.x) reinterpret_cast<float*>(scratch)[i] = 0.0f;
+    __syncthreads();
+  }
+  const Rows<T, WARP, CH, ALIGNED> R(a.M, a.D, ring, 1 + a.has_r);
+  const bool wbf16 = a.wdtype == QLORA_DT_BF16;
   griddep_launch_dependents();
   griddep_wait();
+  auto issue = [&](int64_t row, uint32_t stage) {
+    if (row < a.M) {
+      R.copy(a.X, row * a.D, 0, stage);
+      if (a.has_r) R.copy(a.R, row * a.D, 1, stage);
+    }
+    cp_async_commit();
+  };
+  for (int s = 0; s < a.stages; ++s) issue(R.row0 + s * R.stride, s * R.stage_bytes);
+  f2 w[CH][H], b[CH][H];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) load_w<2 * H>(a.w, wbf16, R.col(c), a.D, w[c]);
+  if (a.has_b) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) load_w<2 * H>(a.b, wbf16, R.col(c), a.D, b[c]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int i = 0; i < H; ++i) b[c][i] = 0;
+  }
+  int stage = 0, buf = 0;
 #pragma unroll 1
-  for (int64_t row = row0; row < a.M; row += static_cast<int64_t>(gridDim.x) * ROWS) {
+  for (int64_t row = R.row0; row < a.M; row += R.stride) {
     const int64_t at = row * a.D;
-    const int sh = ALIGNED ? 0 : static_cast<int>(at % N);
-    const T* x = reinterpret_cast<const T*>(a.X) + at;
-    // all of the row's loads before their first use: S may be R's memory, so the
-    // compiler would keep a window's load behind the store of the one before
-    float v[CH][N];
-    uint4 raw[CH];
+    const uint32_t here = stage * R.stage_bytes;
+    cp_async_wait(a.stages - 1);
+    f2 v[CH][H];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) raw[c] = load_raw<T, ALIGNED>(x, (t + c * NT) * N - sh, a.D);
+    for (int c = 0; c < CH; ++c) unpack2(R.get(0, c, here), v[c], T());
     if (a.has_r) {
-      const T* r = reinterpret_cast<const T*>(a.R) + at;
       T* s = reinterpret_cast<T*>(a.S) + at;
-      uint4 q[CH];
-#pragma unroll
-      for (int c = 0; c < CH; ++c) q[c] = load_raw<T, ALIGNED>(r, (t + c * NT) * N - sh, a.D);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        float f[N];
-        Vec<T>::unpack(raw[c], v[c]);
-        Vec<T>::unpack(q[c], f);
+        f2 q[H];
+        unpack2(R.get(1, c, here), q, T());
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[c][i] += f[i];
-        raw[c] = Vec<T>::pack(v[c]);
-        store_raw<T, ALIGNED>(s, (t + c * NT) * N - sh, a.D, raw[c]);
+        for (int i = 0; i < H; ++i) v[c][i] = f2_add(v[c][i], q[i]);
+        const uint4 packed = pack2(v[c], T());
+        unpack2(packed, v[c], T());
+        store_raw<T, ALIGNED>(s, R.col(c), a.D, packed);
       }
     }
+    issue(row + a.stages * R.stride, here);
+    if constexpr (!ALIGNED) {
+      if (R.col(0) < 0) {   // values of the row before
+        float lo, hi;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) Vec<T>::unpack(raw[c], v[c]);
+        for (int i = 0; i < H; ++i) {
+          f2_get(v[0][i], lo, hi);
+          v[0][i] = f2_make(2 * i < R.sh ? 0.0f : lo, 2 * i + 1 < R.sh ? 0.0f : hi);
+        }
+      }
+    }
     float mean = 0.0f;
     if (!a.rms) {
-      float sum = 0.0f;
+      f2 sum = 0;
 #pragma unroll
       for (int c = 0; c < CH; ++c)
 #pragma unroll
-        for (int i = 0; i < N; ++i) sum += v[c][i];
-      mean = cta_sum<NT>(sum, scratch, 0) / static_cast<float>(a.D);
-    }
-    float sq = 0.0f;
+        for (int i = 0; i < H; ++i) sum = f2_add(sum, v[c][i]);
+      mean = row_sum<WARP, MAXW>(f2_sum(sum), scratch[buf]) / static_cast<float>(a.D);
+      buf ^= 1;
+      const f2 minus = f2_dup(-mean);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int col = (t + c * NT) * N - sh;
+      for (int c = 0; c < CH; ++c) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const bool in = ALIGNED ? col < a.D : (col + i >= 0 && col + i < a.D);
-        v[c][i] = in ? v[c][i] - mean : 0.0f;
-        sq = fmaf(v[c][i], v[c][i], sq);
+        for (int i = 0; i < H; ++i) v[c][i] = f2_add(v[c][i], minus);
+        if (ALIGNED ? R.bytes(c) == 0 : R.bytes(c) < 16 || R.col(c) < 0) {   // outside the row: no share of the variance
+          float lo, hi;
+#pragma unroll
+          for (int i = 0; i < H; ++i) {
+            f2_get(v[c][i], lo, hi);
+            v[c][i] = f2_make(R.in(c, 2 * i) ? lo : 0.0f, R.in(c, 2 * i + 1) ? hi : 0.0f);
+          }
+        }
       }
     }
-    const float rstd = 1.0f / sqrtf(cta_sum<NT>(sq, scratch, 1) / static_cast<float>(a.D) + a.eps);
-    if (t == 0) {
+    f2 sq = 0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int i = 0; i < H; ++i) sq = f2_fma(v[c][i], v[c][i], sq);
+    const float rstd = 1.0f / sqrtf(row_sum<WARP, MAXW>(f2_sum(sq), scratch[buf]) / static_cast<float>(a.D) + a.eps);
+    buf ^= 1;
+    if (R.t == 0) {
       if (a.mean_out) a.mean_out[row] = mean;
       if (a.rstd_out) a.rstd_out[row] = rstd;
     }
     T* y = reinterpret_cast<T*>(a.Y) + at;
+    const f2 scale = f2_dup(rstd);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int col = (t + c * NT) * N - sh;
-      if (col >= a.D) continue;
-      float w[N];
-      load_w<N>(a.w, a.wdtype == QLORA_DT_BF16, col, a.D, w);
+      f2 o[H];
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[c][i] = v[c][i] * rstd * w[i];
-      if (a.has_b) {
-        load_w<N>(a.b, a.wdtype == QLORA_DT_BF16, col, a.D, w);
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[c][i] += w[i];
-      }
-      store_raw<T, ALIGNED>(y, col, a.D, Vec<T>::pack(v[c]));
+      for (int i = 0; i < H; ++i) o[i] = f2_fma(f2_mul(v[c][i], scale), w[c][i], b[c][i]);
+      store_raw<T, ALIGNED>(y, R.col(c), a.D, pack2(o, T()));
     }
-    if constexpr (NT != 32) {
-      // rms uses one reduction per row: keep the next row's from this row's reads
-      if (a.rms) __syncthreads();
-    }
+    stage = stage + 1 == a.stages ? 0 : stage + 1;
   }
+  cp_async_wait(0);
 }
 
 // ---------------------------------------------------------------------------
-// Backward.  A CTA (or warp) walks over rows gridDim apart.  Its threads keep
-// the same columns for every row, so the weight's gradient is summed in
-// registers and leaves them once, as one row of partial sums per CTA;
-// k_norm_reduce adds those in a fixed order.  Rows that do not start on 16-byte
-// boundaries shift the windows; the grid is then a multiple of N rows apart, so
-// a thread's columns still never change.
-//
-// The rows' loads run a.stages rows ahead through a ring in shared memory
-// (cp.async): registers hold the gradient's sums and cannot hold rows in
-// flight as well.  Each thread reads back only the 16-byte slots that it filled
-// itself, so the ring needs no barrier; the one barrier per row belongs to the
-// row's two sums.  Rows above 8192 values are held by a pair of CTAs (a cluster
-// of two SMs), which exchange those sums through each other's shared memory: one
-// CTA of 1024 threads would have 64 registers per thread and spill the sums.
+// Backward.  Each CTA leaves the weight's gradient of its rows as one row of
+// partial sums; k_norm_reduce adds those in a fixed order.  With the bias's
+// gradient in registers as well, the weight moves to shared memory.
 // ---------------------------------------------------------------------------
-constexpr int bwd_ctas(int nt, int e) { return nt == 32 ? (e > 8 ? 4 : 6) : nt == 64 ? 8 : nt == 128 ? 4 : nt == 256 ? 2 : 1; }
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// a float into this CTA's shared memory and into the pair's other CTA's
-__device__ __forceinline__ void st_pair(float* p, float v, uint32_t other) {
-  *p = v;
-  uint32_t remote;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(p)), "r"(other));
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(v) : "memory");
-}
-
-template <typename T, int NT, int CH, bool ALIGNED, bool DB, bool PAIR>
-__global__ void __launch_bounds__(NT == 32 ? 128 : NT, bwd_ctas(NT, CH * Vec<T>::N)) k_norm_bwd(NormArgs a) {
-  constexpr int N = Vec<T>::N;
-  constexpr int ROWS = NT == 32 ? 4 : 1;
-  constexpr int TB = NT == 32 ? 128 : NT;     // threads of the CTA
-  constexpr int STEP = PAIR ? 2 * NT : NT;    // threads of a row
-  __shared__ float scratch[128];
+template <typename T, int MAXT, int CH, bool ALIGNED, bool DB>
+__global__ void __launch_bounds__(MAXT, norm_ctas(MAXT)) k_norm_bwd(NormArgs a) {
+  constexpr int N = Vec<T>::N, H = N / 2;
+  constexpr int WV = N / 4;                   // 16-byte slots of a window's fp32 weights
+  constexpr int MAXW = MAXT / 32;
+  constexpr bool WARP = MAXT == 128;
+  using Row = Rows<T, WARP, CH, ALIGNED>;
+  __shared__ float4 scratch[2][MAXW / 2];
   extern __shared__ __align__(16) uint8_t ring[];
-  const int half = PAIR ? (blockIdx.x & 1) : 0;
-  const int t = NT == 32 ? (threadIdx.x & 31) : threadIdx.x + half * NT;
-  const int r = NT == 32 ? (threadIdx.x >> 5) : 0;
-  const int64_t row0 = static_cast<int64_t>(PAIR ? blockIdx.x >> 1 : blockIdx.x) * ROWS + r;
-  const int64_t stride = static_cast<int64_t>(PAIR ? gridDim.x >> 1 : gridDim.x) * ROWS;
-  const uint32_t slot0 = smem_u32(ring) + threadIdx.x * 16u;
-  const int arrays = 2 + a.has_ds;
-  const uint32_t stage_bytes = static_cast<uint32_t>(arrays * CH * TB * 16);
+  if constexpr (!WARP) {
+    for (int i = threadIdx.x; i < 4 * MAXW; i += blockDim.x) reinterpret_cast<float*>(scratch)[i] = 0.0f;
+    __syncthreads();
+  }
+  const Row R(a.M, a.D, ring, 2 + a.ring_ds);
+  const bool wbf16 = a.wdtype == QLORA_DT_BF16;
+  const uint32_t wslot = R.slot0 + a.stages * R.stage_bytes;
   griddep_launch_dependents();
   griddep_wait();
-  const int sh = ALIGNED ? 0 : static_cast<int>((row0 * a.D) % N);
-  const bool wbf16 = a.wdtype == QLORA_DT_BF16;
-
-  // window c of the row: what it can read of the row (a window past the row's
-  // end reads nothing, one that starts in the row before reads that too)
   auto issue = [&](int64_t row, uint32_t stage) {
     if (row < a.M) {
-      const int64_t at = row * a.D;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int col = (t + c * STEP) * N - sh;
-        const int bytes = min(max(a.D - col, 0), N) * static_cast<int>(sizeof(T));
-        const int64_t src = at + (bytes ? col : 0);
-        const uint32_t dst = slot0 + stage + static_cast<uint32_t>(c * TB * 16);
-        cp_async16(dst, reinterpret_cast<const T*>(a.X) + (bytes ? src : at - sh), bytes);
-        cp_async16(dst + CH * TB * 16, reinterpret_cast<const T*>(a.dY) + (bytes ? src : at - sh), bytes);
-        if (a.has_ds)
-          cp_async16(dst + 2 * CH * TB * 16, reinterpret_cast<const T*>(a.dS) + (bytes ? src : at - sh), bytes);
-      }
+      R.copy(a.X, row * a.D, 0, stage);
+      R.copy(a.dY, row * a.D, 1, stage);
+      if (a.ring_ds) R.copy(a.dS, row * a.D, 2, stage);
     }
     cp_async_commit();
   };
-
-  float dw[CH][N], db[DB ? CH : 1][N], w[CH][N];
+  for (int s = 0; s < a.stages; ++s) issue(R.row0 + s * R.stride, s * R.stage_bytes);
+  f2 dw[CH][H], db[DB ? CH : 1][H], w[DB ? 1 : CH][H];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    load_w<N>(a.w, wbf16, (t + c * STEP) * N - sh, a.D, w[c]);
+    f2 q[H];
+    load_w<N>(a.w, wbf16, R.col(c), a.D, q);
 #pragma unroll
-    for (int i = 0; i < N; ++i) dw[c][i] = 0.0f;
+    for (int i = 0; i < H; ++i) {
+      dw[c][i] = 0;
+      if constexpr (DB)
+        db[c][i] = 0;
+      else
+        w[c][i] = q[i];
+    }
     if constexpr (DB)
 #pragma unroll
-      for (int i = 0; i < N; ++i) db[c][i] = 0.0f;
+      for (int k = 0; k < WV; ++k) {
+        const f2 p[2] = {q[2 * k], q[2 * k + 1]};
+        sts128(wslot + (c * WV + k) * R.tb * 16, pack2(p, 0.0f));
+      }
   }
-  for (int s = 0; s < a.stages; ++s) issue(row0 + s * stride, s * stage_bytes);
-  if constexpr (PAIR) cluster_sync();   // both CTAs run before either writes to the other
+  auto weight = [&](int c, f2 (&q)[H]) {
+#pragma unroll
+    for (int k = 0; k < WV; ++k) {
+      f2 p[2];
+      unpack2(lds128(wslot + (c * WV + k) * R.tb * 16), p, 0.0f);
+      q[2 * k] = p[0];
+      q[2 * k + 1] = p[1];
+    }
+  };
 
   const float inv_d = 1.0f / static_cast<float>(a.D);
   float mean = 0.0f, rstd = 0.0f;
-  if (row0 < a.M) {
-    mean = a.mean_in[row0];
-    rstd = a.rstd_in[row0];
+  if (R.row0 < a.M) {
+    mean = a.mean_in[R.row0];
+    rstd = a.rstd_in[R.row0];
   }
   int buf = 0, stage = 0;
 #pragma unroll 1
-  for (int64_t row = row0; row < a.M; row += stride, buf ^= 1) {
-    const int64_t next = min(row + stride, a.M - 1);
+  for (int64_t row = R.row0; row < a.M; row += R.stride, buf ^= 1) {
+    const int64_t next = min(row + R.stride, a.M - 1);
     const float mean_next = a.mean_in[next], rstd_next = a.rstd_in[next];
     if (a.rms) mean = 0.0f;
-    const uint32_t slot = slot0 + stage * stage_bytes;
+    const uint32_t here = stage * R.stage_bytes;
     cp_async_wait(a.stages - 1);
-    // xh and g = dY w of window c
-    auto take = [&](int c, float (&xh)[N], float (&dy)[N]) {
-      Vec<T>::unpack(lds128(slot + c * TB * 16), xh);
-      Vec<T>::unpack(lds128(slot + (CH + c) * TB * 16), dy);
-      if (!ALIGNED && c == 0 && t * N - sh < 0) {   // values of the row before
+    const f2 minus = f2_dup(-mean), scale = f2_dup(rstd);
+    // xh and dY of window c
+    auto take = [&](int c, f2 (&xh)[H], f2 (&dy)[H]) {
+      unpack2(R.get(0, c, here), xh, T());
+      unpack2(R.get(1, c, here), dy, T());
+      if (!ALIGNED && c == 0 && R.col(0) < 0) {   // values of the row before
+        float lo, hi;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (i < sh) xh[i] = dy[i] = 0.0f;
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i) xh[i] = (xh[i] - mean) * rstd;
-    };
-    float c1 = 0.0f, c2 = 0.0f;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      float xh[N], dy[N];
-      take(c, xh, dy);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        // outside the row dY and w are zero, so whatever xh is there adds nothing
-        dw[c][i] = fmaf(dy[i], xh[i], dw[c][i]);
-        if constexpr (DB) db[c][i] += dy[i];
-        const float g = dy[i] * w[c][i];
-        c1 += g;
-        c2 = fmaf(g, xh[i], c2);
-      }
-    }
-    c1 = warp_sum(c1);
-    c2 = warp_sum(c2);
-    if constexpr (NT != 32) {
-      constexpr int NW = STEP / 32;
-      float* s = scratch + buf * 64;
-      if ((threadIdx.x & 31) == 0) {
-        const int at = t >> 5;
-        if constexpr (PAIR) {
-          st_pair(s + at, c1, half ^ 1);
-          st_pair(s + 32 + at, c2, half ^ 1);
-        } else {
-          s[at] = c1;
-          s[32 + at] = c2;
+        for (int i = 0; i < H; ++i) {
+          f2_get(xh[i], lo, hi);
+          xh[i] = f2_make(2 * i < R.sh ? 0.0f : lo, 2 * i + 1 < R.sh ? 0.0f : hi);
+          f2_get(dy[i], lo, hi);
+          dy[i] = f2_make(2 * i < R.sh ? 0.0f : lo, 2 * i + 1 < R.sh ? 0.0f : hi);
         }
       }
-      if constexpr (PAIR) {
-        __syncwarp();
-        cluster_sync();
-      } else {
-        __syncthreads();
-      }
-      c1 = c2 = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NW; ++i) {
-        c1 += s[i];
-        c2 += s[32 + i];
+      for (int i = 0; i < H; ++i) xh[i] = f2_mul(f2_add(xh[i], minus), scale);
+    };
+    f2 c1 = 0, c2 = 0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      f2 xh[H], dy[H], wl[H];
+      take(c, xh, dy);
+      if constexpr (DB) weight(c, wl);
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        // outside the row dY and w are zero, so whatever xh is there adds nothing
+        dw[c][i] = f2_fma(dy[i], xh[i], dw[c][i]);
+        if constexpr (DB) db[c][i] = f2_add(db[c][i], dy[i]);
+        const f2 g = f2_mul(dy[i], DB ? wl[i] : w[DB ? 0 : c][i]);
+        c1 = f2_add(c1, g);
+        c2 = f2_fma(g, xh[i], c2);
       }
     }
-    c1 = a.rms ? 0.0f : c1 * inv_d;
-    c2 *= inv_d;
+    float m1, m2;
+    f2_get(row_sum2<WARP, MAXW>(f2_sum(c1), f2_sum(c2), scratch[buf]), m1, m2);
     if (a.dX) {
+      const f2 off = f2_dup(a.rms ? 0.0f : -m1 * inv_d), along = f2_dup(-m2 * inv_d);
       T* dx = reinterpret_cast<T*>(a.dX) + row * a.D;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int col = (t + c * STEP) * N - sh;
-        float xh[N], o[N];
+        f2 xh[H], o[H], q[H];
         take(c, xh, o);
+        if constexpr (DB) weight(c, q);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float g = o[i] * w[c][i];
-          o[i] = rstd * (g - c1 - xh[i] * c2);
-        }
+        for (int i = 0; i < H; ++i)
+          o[i] = f2_fma(xh[i], along, f2_fma(o[i], DB ? q[i] : w[DB ? 0 : c][i], off));
         if (a.has_ds) {
-          float q[N];
-          Vec<T>::unpack(lds128(slot + (2 * CH + c) * TB * 16), q);
+          const T* ds = reinterpret_cast<const T*>(a.dS) + row * a.D;
+          unpack2(a.ring_ds ? R.get(2, c, here) : load_raw<T, ALIGNED>(ds, R.col(c), a.D), q, T());
 #pragma unroll
-          for (int i = 0; i < N; ++i) o[i] += q[i];
+          for (int i = 0; i < H; ++i) o[i] = f2_fma(o[i], scale, q[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < H; ++i) o[i] = f2_mul(o[i], scale);
         }
-        store_raw<T, ALIGNED>(dx, col, a.D, Vec<T>::pack(o));
+        store_raw<T, ALIGNED>(dx, R.col(c), a.D, pack2(o, T()));
       }
     }
-    issue(row + a.stages * stride, stage * stage_bytes);
+    issue(row + a.stages * R.stride, here);
     stage = stage + 1 == a.stages ? 0 : stage + 1;
     mean = mean_next;
     rstd = rstd_next;
   }
   cp_async_wait(0);
-  __syncwarp();
-  if constexpr (PAIR) cluster_sync();   // neither CTA leaves while the other may still write to it
-  // one row of partial sums per CTA (or pair)
-  float* part = a.part + static_cast<int64_t>(PAIR ? blockIdx.x >> 1 : blockIdx.x) * a.D * (DB ? 2 : 1);
+  // one row of partial sums per CTA
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * a.D * (DB ? 2 : 1);
 #pragma unroll
   for (int k = 0; k < (DB ? 2 : 1); ++k) {
-    if constexpr (NT == 32) {
-      // the four warps' sums, added in order: the ring is free for them now
-      float* comb = reinterpret_cast<float*>(ring);
+    // the four warps' sums are added in order: the ring is free for them now
+    float* comb = WARP ? reinterpret_cast<float*>(ring) : part + k * a.D;
+    if constexpr (WARP) {
       __syncthreads();
       for (int j = threadIdx.x; j < a.D; j += 128) comb[j] = 0.0f;
-      for (int rr = 0; rr < ROWS; ++rr) {
-        __syncthreads();
-        if (rr == r) {
+    }
+    for (int rr = 0; rr < Row::ROWS; ++rr) {
+      if constexpr (WARP) __syncthreads();
+      if (rr == R.r) {
 #pragma unroll
-          for (int c = 0; c < CH; ++c)
+        for (int c = 0; c < CH; ++c)
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const int col = (t + c * STEP) * N - sh + i;
-              if (col >= 0 && col < a.D) comb[col] += k ? db[DB ? c : 0][i] : dw[c][i];
-            }
-        }
+          for (int i = 0; i < N; ++i) {
+            float lo, hi;
+            f2_get(k ? db[DB ? c : 0][i / 2] : dw[c][i / 2], lo, hi);
+            const int col = R.col(c) + i;
+            if (R.in(c, i)) comb[col] = (WARP ? comb[col] : 0.0f) + (i & 1 ? hi : lo);
+          }
       }
+    }
+    if constexpr (WARP) {
       __syncthreads();
       for (int j = threadIdx.x; j < a.D; j += 128) part[k * a.D + j] = comb[j];
-    } else {
-#pragma unroll
-      for (int c = 0; c < CH; ++c)
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int col = (t + c * STEP) * N - sh + i;
-          if (col >= 0 && col < a.D) part[k * a.D + col] = k ? db[DB ? c : 0][i] : dw[c][i];
-        }
     }
   }
 }
@@ -413,145 +482,129 @@ __global__ void __launch_bounds__(1024) k_norm_reduce(const float* part, int P, 
 }
 
 struct Cfg {
-  int nt, e;   // threads per row, values per thread
+  int maxt, e, nt;   // kernel variant (most threads; 128: a warp per row), values per thread, threads of the CTA
 };
 
-// Forward: as few threads per row as hold it with 16 to 32 values each, so that
-// several rows are in flight on an SM; for no more rows than SMs the row is
-// spread over up to 1024 threads, for latency.
-Cfg fwd_cfg(int64_t need, int64_t M) {
-  if (need <= 256) return {32, 8};
-  if (M <= num_sms()) {
-    if (need <= 8192) return {1024, 8};
-    return {1024, 17};
-  }
-  if (need <= 512) return {32, 16};
-  if (need <= 1024) return {32, 32};
-  if (need <= 2048) return {128, 16};
-  if (need <= 4096) return {256, 16};
-  if (need <= 8192) return {256, 32};
-  return {544, 32};
+// 32 values per thread where the row is long enough, in as many warps as it
+// takes, up to 8192 values; longer rows always have 512 threads, since an SM
+// holds one such CTA.  (The last case: unaligned rows next to the limit.)  A
+// forward pass over no more rows than SMs spreads a long row over 1024 threads,
+// for latency.
+Cfg norm_cfg(int64_t need, int64_t M, bool fwd) {
+  if (need <= 256) return {128, 8, 128};
+  if (need <= 512) return {128, 16, 128};
+  if (fwd && M <= num_sms() && need > 2048 && need <= 16384) return {1024, need <= 8192 ? 8 : 16, 1024};
+  if (fwd && need <= 1024) return {128, 32, 128};   // backward: a warp could not hold both gradients' sums
+  if (need <= 8192) return {512, 32, static_cast<int>(align_up(ceil_div(need, 32), 32))};
+  return need <= 16384 ? Cfg{512, 32, 512} : Cfg{512, 40, 416};
 }
 
-Cfg bwd_cfg(int64_t need) {
-  if (need <= 256) return {32, 8};
-  if (need <= 512) return {32, 16};
-  if (need <= 1024) return {64, 16};
-  if (need <= 2048) return {128, 16};
-  if (need <= 4096) return {256, 16};
-  if (need <= 8192) return {512, 16};
-  if (need <= 16384) return {1024, 16};   // a pair of 512
-  return {1024, 17};
-}
-
-template <typename T, int NT, int E>
-cudaError_t run_fwd(const NormArgs& a, bool aligned, cudaStream_t st) {
-  constexpr int CH = (E + Vec<T>::N - 1) / Vec<T>::N;
-  constexpr int ROWS = NT == 32 ? 4 : 1;
-  const dim3 block(NT == 32 ? 128 : NT);
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ceil_div(a.M, ROWS), int64_t(1) << 30)));
-  ProfScope prof(QLORA_KC_AUX, st);
-  return aligned ? launch_pdl(k_norm_fwd<T, NT, CH, true>, grid, block, 0, st, nullptr, a)
-                 : launch_pdl(k_norm_fwd<T, NT, CH, false>, grid, block, 0, st, nullptr, a);
-}
-
-template <typename T>
-cudaError_t pick_fwd(const NormArgs& a, cudaStream_t st) {
-  const bool aligned = a.D % Vec<T>::N == 0;
-  const Cfg c = fwd_cfg(a.D + (aligned ? 0 : Vec<T>::N - 1), a.M);
-  switch (c.nt * 64 + c.e) {
-    case 32 * 64 + 8: return run_fwd<T, 32, 8>(a, aligned, st);
-    case 32 * 64 + 16: return run_fwd<T, 32, 16>(a, aligned, st);
-    case 32 * 64 + 32: return run_fwd<T, 32, 32>(a, aligned, st);
-    case 128 * 64 + 16: return run_fwd<T, 128, 16>(a, aligned, st);
-    case 256 * 64 + 16: return run_fwd<T, 256, 16>(a, aligned, st);
-    case 256 * 64 + 32: return run_fwd<T, 256, 32>(a, aligned, st);
-    case 1024 * 64 + 8: return run_fwd<T, 1024, 8>(a, aligned, st);
-    case 1024 * 64 + 17: return run_fwd<T, 1024, 17>(a, aligned, st);
-    default: return run_fwd<T, 544, 32>(a, aligned, st);
-  }
-}
-
-template <typename T, int NTROW, int E, bool ALIGNED, bool DB>
-cudaError_t run_bwd3(NormArgs a, int grid, cudaStream_t st) {
-  constexpr bool PAIR = NTROW == 1024;
-  constexpr int NT = PAIR ? 512 : NTROW;
-  constexpr int CH = (E + Vec<T>::N - 1) / Vec<T>::N;
-  constexpr int TB = NT == 32 ? 128 : NT;
-  // as many rows ahead as fit beside the SM's other CTAs, four at most
-  const uint32_t stage = static_cast<uint32_t>((2 + a.has_ds) * CH * TB * 16);
-  const uint32_t room = 200u * 1024u / bwd_ctas(NT, CH * Vec<T>::N);
-  a.stages = static_cast<int>(std::min(4u, std::max(1u, room / stage)));
-  const uint32_t smem = std::max(stage * a.stages, NT == 32 ? static_cast<uint32_t>(a.D) * 4u : 0u);
-  auto kernel = k_norm_bwd<T, NT, CH, ALIGNED, DB, PAIR>;
-  cudaError_t e = set_smem(kernel, smem);
-  if (e != cudaSuccess) return e;
-  ProfScope prof(QLORA_KC_AUX, st);
-  const dim3 pair(2, 1, 1);
-  return launch_pdl(kernel, dim3(PAIR ? 2 * grid : grid), dim3(TB), smem, st, PAIR ? &pair : nullptr, a);
-}
-
-template <typename T, int NT, int E>
-cudaError_t run_bwd(const NormArgs& a, bool aligned, int grid, cudaStream_t st) {
-  if (a.db) return aligned ? run_bwd3<T, NT, E, true, true>(a, grid, st) : run_bwd3<T, NT, E, false, true>(a, grid, st);
-  return aligned ? run_bwd3<T, NT, E, true, false>(a, grid, st) : run_bwd3<T, NT, E, false, false>(a, grid, st);
-}
-
-// CTAs (or pairs) of the backward pass: what fits on the SMs, no more than there
-// are rows; each leaves one row of partial sums.
-// Unaligned rows with several rows per CTA: a multiple of 8, so that the rows a
-// CTA visits start at the same offset from a 16-byte boundary.
-int bwd_grid(int64_t M, int64_t D, int n) {
-  const Cfg c = bwd_cfg(D + (D % n ? n - 1 : 0));
-  const int rows = c.nt == 32 ? 4 : 1;
-  const int64_t want = ceil_div(M, rows);
-  int64_t g = c.nt == 1024 ? num_sms() / 2 : static_cast<int64_t>(num_sms()) * bwd_ctas(c.nt, c.e);
-  if (D % n) g = g / 8 * 8;
+// CTAs: what fits on the SMs, no more than there are rows.  The forward pass
+// takes several times as many where a CTA still gets three rows: SMs differ in
+// the bandwidth they get, and the SMs that are ahead then take more of the CTAs
+// (8192 x 8192 bf16: with the residual 95 us at one wave, 85 at four, 82 at
+// eight; without 53 at one, 52 at two, 60 at eight).  Unaligned rows with several
+// rows per CTA: a multiple of 8, so that the rows that a CTA visits start at the
+// same offset from a 16-byte boundary.
+int norm_grid(int64_t M, int64_t D, int n, bool fwd, bool residual) {
+  const Cfg c = norm_cfg(D + (D % n ? n - 1 : 0), M, fwd);
+  const int64_t want = ceil_div(M, c.maxt == 128 ? 4 : 1);
+  int64_t g = static_cast<int64_t>(num_sms()) * norm_ctas(c.nt);
+  if (fwd) g *= std::max<int64_t>(1, std::min<int64_t>(residual ? 8 : 2, want / (3 * g)));
+  if (D % n) g = std::max<int64_t>(8, g / 8 * 8);
   return static_cast<int>(std::max<int64_t>(1, std::min(want, g)));
 }
 
-template <typename T>
-cudaError_t pick_bwd(const NormArgs& a, cudaStream_t st) {
-  const bool aligned = a.D % Vec<T>::N == 0;
-  const Cfg c = bwd_cfg(a.D + (aligned ? 0 : Vec<T>::N - 1));
-  const int grid = bwd_grid(a.M, a.D, Vec<T>::N);
-  cudaError_t e;
-  switch (c.nt * 64 + c.e) {
-    case 32 * 64 + 8: e = run_bwd<T, 32, 8>(a, aligned, grid, st); break;
-    case 32 * 64 + 16: e = run_bwd<T, 32, 16>(a, aligned, grid, st); break;
-    case 64 * 64 + 16: e = run_bwd<T, 64, 16>(a, aligned, grid, st); break;
-    case 128 * 64 + 16: e = run_bwd<T, 128, 16>(a, aligned, grid, st); break;
-    case 256 * 64 + 16: e = run_bwd<T, 256, 16>(a, aligned, grid, st); break;
-    case 512 * 64 + 16: e = run_bwd<T, 512, 16>(a, aligned, grid, st); break;
-    case 1024 * 64 + 16: e = run_bwd<T, 1024, 16>(a, aligned, grid, st); break;
-    default: e = run_bwd<T, 1024, 17>(a, aligned, grid, st); break;
-  }
+constexpr uint32_t kNormRoom = 215u * 1024u;   // dynamic shared memory of an SM's CTAs together, 1 KB less each
+
+// Rows ahead, as many as fit beside the SM's other CTAs, four at most; `fixed`
+// bytes of shared memory follow the ring.
+template <typename K>
+cudaError_t launch_rows(K kernel, NormArgs a, int grid, int nt, uint32_t stage, uint32_t fixed, uint32_t least,
+                        cudaStream_t st) {
+  const uint32_t room = (kNormRoom + 1024u) / static_cast<uint32_t>(norm_ctas(nt)) - 1024u;
+  a.stages = static_cast<int>(std::min(4u, std::max(1u, room > fixed ? (room - fixed) / stage : 0u)));
+  const uint32_t smem = std::max(stage * a.stages + fixed, least);
+  cudaError_t e = set_smem(kernel, smem);
   if (e != cudaSuccess) return e;
-  const int64_t cols = a.D * (a.db ? 2 : 1);
+  ProfScope prof(QLORA_KC_AUX, st);
+  return launch_pdl(kernel, dim3(grid), dim3(nt), smem, st, nullptr, a);
+}
+
+template <typename T, int MAXT, int E>
+struct Fwd {
+  static cudaError_t run(const NormArgs& a, int grid, int nt, cudaStream_t st) {
+    constexpr int CH = E / Vec<T>::N;
+    const uint32_t stage = static_cast<uint32_t>((1 + a.has_r) * CH * nt * 16);
+    return launch_rows(a.D % Vec<T>::N == 0 ? k_norm_fwd<T, MAXT, CH, true> : k_norm_fwd<T, MAXT, CH, false>, a, grid,
+                       nt, stage, 0, 0, st);
+  }
+};
+
+template <typename T, int MAXT, int E>
+struct Bwd {
+  static cudaError_t run(const NormArgs& a, int grid, int nt, cudaStream_t st) {
+    constexpr int CH = E / Vec<T>::N;
+    NormArgs b = a;
+    // fp32 rows above 8192 values: no room for dS in the ring
+    const uint32_t array = static_cast<uint32_t>(CH * nt * 16), fixed = a.db ? nt * E * 4 : 0;
+    b.ring_ds = a.has_ds && 3 * array + fixed <= (kNormRoom + 1024u) / norm_ctas(nt) - 1024u;
+    const uint32_t stage = (2 + b.ring_ds) * array;
+    const bool al = a.D % Vec<T>::N == 0;
+    auto kernel = a.db ? (al ? k_norm_bwd<T, MAXT, CH, true, true> : k_norm_bwd<T, MAXT, CH, false, true>)
+                       : (al ? k_norm_bwd<T, MAXT, CH, true, false> : k_norm_bwd<T, MAXT, CH, false, false>);
+    return launch_rows(kernel, b, grid, nt, stage, fixed, MAXT == 128 ? static_cast<uint32_t>(a.D) * 4u : 0u, st);
+  }
+};
+
+// the variants that both passes have
+template <typename T, template <typename, int, int> class K>
+cudaError_t pick(const Cfg& c, const NormArgs& a, int grid, cudaStream_t st) {
+  if (c.maxt == 128) return c.e == 8 ? K<T, 128, 8>::run(a, grid, c.nt, st) : K<T, 128, 16>::run(a, grid, c.nt, st);
+  return c.e == 32 ? K<T, 512, 32>::run(a, grid, c.nt, st) : K<T, 512, 40>::run(a, grid, c.nt, st);
+}
+
+template <typename T>
+cudaError_t run_fwd(const NormArgs& a, cudaStream_t st) {
+  constexpr int N = Vec<T>::N;
+  const Cfg c = norm_cfg(a.D + (a.D % N ? N - 1 : 0), a.M, true);
+  const int grid = norm_grid(a.M, a.D, N, true, a.has_r);
+  if (c.maxt == 1024)
+    return c.e == 8 ? Fwd<T, 1024, 8>::run(a, grid, c.nt, st) : Fwd<T, 1024, 16>::run(a, grid, c.nt, st);
+  if (c.maxt == 128 && c.e == 32) return Fwd<T, 128, 32>::run(a, grid, c.nt, st);
+  return pick<T, Fwd>(c, a, grid, st);
+}
+
+cudaError_t reduce(const NormArgs& a, int parts, cudaStream_t st) {
+  const int64_t cols = static_cast<int64_t>(a.D) * (a.db ? 2 : 1);
   ProfScope prof(QLORA_KC_AUX, st);
   return launch_pdl(k_norm_reduce, dim3(static_cast<unsigned>(ceil_div(cols, 32))), dim3(1024), 0, st, nullptr,
-                    static_cast<const float*>(a.part), grid, cols, static_cast<int64_t>(a.D), a.dw, a.db);
+                    static_cast<const float*>(a.part), parts, cols, static_cast<int64_t>(a.D), a.dw, a.db);
+}
+
+template <typename T>
+cudaError_t run_bwd(const NormArgs& a, cudaStream_t st) {
+  constexpr int N = Vec<T>::N;
+  const int grid = norm_grid(a.M, a.D, N, false, false);
+  cudaError_t e = pick<T, Bwd>(norm_cfg(a.D + (a.D % N ? N - 1 : 0), a.M, false), a, grid, st);
+  return e != cudaSuccess ? e : reduce(a, grid, st);
 }
 
 }  // namespace
 
 size_t norm_workspace_bytes(int64_t M, int64_t D, int dtype, bool dbias) {
   if (M == 0) return 0;
-  return align_up(static_cast<size_t>(bwd_grid(M, D, dtype == QLORA_DT_BF16 ? 8 : 4)) * D * (dbias ? 2 : 1) * 4, 256);
+  return align_up(static_cast<size_t>(norm_grid(M, D, dtype == QLORA_DT_BF16 ? 8 : 4, false, false)) * D * (dbias ? 2 : 1) * 4,
+                  256);
 }
 
 cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t st) {
-  return a.dtype == QLORA_DT_BF16 ? pick_fwd<__nv_bfloat16>(a, st) : pick_fwd<float>(a, st);
+  return a.dtype == QLORA_DT_BF16 ? run_fwd<__nv_bfloat16>(a, st) : run_fwd<float>(a, st);
 }
 
 cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t st) {
-  if (a.M == 0) {   // no rows: the sums are zero
-    const int64_t cols = static_cast<int64_t>(a.D) * (a.db ? 2 : 1);
-    ProfScope prof(QLORA_KC_AUX, st);
-    return launch_pdl(k_norm_reduce, dim3(static_cast<unsigned>(ceil_div(cols, 32))), dim3(1024), 0, st, nullptr,
-                      static_cast<const float*>(nullptr), 0, cols, static_cast<int64_t>(a.D), a.dw, a.db);
-  }
-  return a.dtype == QLORA_DT_BF16 ? pick_bwd<__nv_bfloat16>(a, st) : pick_bwd<float>(a, st);
+  if (a.M == 0) return reduce(a, 0, st);   // no rows: the sums are zero
+  return a.dtype == QLORA_DT_BF16 ? run_bwd<__nv_bfloat16>(a, st) : run_bwd<float>(a, st);
 }
 
 }  // namespace qlora

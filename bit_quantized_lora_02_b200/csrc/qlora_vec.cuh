@@ -41,6 +41,63 @@ struct Vec<float> {
   }
 };
 
+// Two fp32 values in one 64-bit register (packed f32x2 arithmetic of sm_100:
+// each half is one IEEE operation, rounded to nearest even).
+using f2 = uint64_t;
+__device__ __forceinline__ f2 f2_make(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f2 f2_dup(float x) { return f2_make(x, x); }
+__device__ __forceinline__ void f2_get(f2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ float f2_sum(f2 v) {
+  float a, b;
+  f2_get(v, a, b);
+  return a + b;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// A 16-byte vector as pairs of fp32.
+__device__ __forceinline__ void unpack2(const uint4& v, f2 (&f)[4], __nv_bfloat16) {
+  f[0] = f2_make(bf16_lo(v.x), bf16_hi(v.x));
+  f[1] = f2_make(bf16_lo(v.y), bf16_hi(v.y));
+  f[2] = f2_make(bf16_lo(v.z), bf16_hi(v.z));
+  f[3] = f2_make(bf16_lo(v.w), bf16_hi(v.w));
+}
+__device__ __forceinline__ void unpack2(const uint4& v, f2 (&f)[2], float) {
+  f[0] = f2_make(__uint_as_float(v.x), __uint_as_float(v.y));
+  f[1] = f2_make(__uint_as_float(v.z), __uint_as_float(v.w));
+}
+__device__ __forceinline__ uint32_t pack2_bf16(f2 v) {
+  float lo, hi;
+  f2_get(v, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
+__device__ __forceinline__ uint4 pack2(const f2 (&f)[4], __nv_bfloat16) {
+  return make_uint4(pack2_bf16(f[0]), pack2_bf16(f[1]), pack2_bf16(f[2]), pack2_bf16(f[3]));
+}
+__device__ __forceinline__ uint4 pack2(const f2 (&f)[2], float) {
+  return make_uint4(static_cast<uint32_t>(f[0]), static_cast<uint32_t>(f[0] >> 32), static_cast<uint32_t>(f[1]),
+                    static_cast<uint32_t>(f[1] >> 32));
+}
+
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 template <typename T>
@@ -103,6 +160,9 @@ __device__ __forceinline__ void cp_async_wait(int left) {
     asm volatile("cp.async.wait_group 1;" ::: "memory");
   else
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
