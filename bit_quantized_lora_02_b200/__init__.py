@@ -33,7 +33,8 @@ EXPORTS = ("qlora_nf4_sizes", "nf4_quantize", "nf4_quantize_noalloc", "nf4_dequa
            "qlora_dropout_mask", "qlora_linear_dropout_workspace_size", "qlora_linear_fwd_dropout",
            "qlora_linear_bwd_dropout", "qlora_selftest_wait_timeout", "qlora_grouped_workspace_size",
            "qlora_linear_fwd_grouped", "qlora_linear_bwd_grouped",
-           "qlora_layer_norm_fwd", "qlora_layer_norm_bwd", "qlora_layer_norm_workspace_size")
+           "qlora_layer_norm_fwd", "qlora_layer_norm_bwd", "qlora_layer_norm_workspace_size",
+           "qlora_adamw_step", "qlora_adamw_state_values")
 
 KERNEL_CLASSES = ("quant", "dq_const", "dequant", "fwd_gemm", "bwd_gemm", "lora_gemm", "aux")
 
@@ -69,6 +70,21 @@ class QloraNorm(ctypes.Structure):
     """Mirror of ``qlora_norm_t``."""
     _fields_ = [("M", ctypes.c_int64), ("D", ctypes.c_int64), ("dtype", ctypes.c_int32), ("wdtype", ctypes.c_int32),
                 ("rms", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class QloraAdamWTensor(ctypes.Structure):
+    """Mirror of ``qlora_adamw_tensor_t``."""
+    _fields_ = [("param", ctypes.c_void_p), ("copy", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class QloraAdamW(ctypes.Structure):
+    """Mirror of ``qlora_adamw_t``."""
+    _fields_ = [("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("state_bits", ctypes.c_int32),
+                ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
+                ("grad_scale", ctypes.c_void_p), ("clock", ctypes.c_void_p)]
 
 
 _lib = None
@@ -113,6 +129,8 @@ def lib() -> ctypes.CDLL:
     L.qlora_layer_norm_fwd.argtypes = [NP, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.qlora_layer_norm_bwd.argtypes = [NP, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, c_sz, vp]
     L.qlora_layer_norm_workspace_size.argtypes = [NP, c_i32, ctypes.POINTER(c_sz)]
+    L.qlora_adamw_step.argtypes = [ctypes.POINTER(QloraAdamW), ctypes.POINTER(QloraAdamWTensor), c_i64, vp]
+    L.qlora_adamw_state_values.argtypes = [c_i64, vp, vp, vp, vp, vp, vp, vp]
     L.qlora_last_error.restype = ctypes.c_char_p
     L.qlora_profile_enable.argtypes = [c_i32]
     L.qlora_profile_read.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64)]
@@ -123,7 +141,7 @@ def lib() -> ctypes.CDLL:
                  "qlora_linear_dropout_workspace_size", "qlora_linear_fwd_dropout", "qlora_linear_bwd_dropout",
                  "qlora_selftest_wait_timeout", "qlora_grouped_workspace_size", "qlora_linear_fwd_grouped",
                  "qlora_linear_bwd_grouped", "qlora_layer_norm_fwd", "qlora_layer_norm_bwd",
-                 "qlora_layer_norm_workspace_size"):
+                 "qlora_layer_norm_workspace_size", "qlora_adamw_step", "qlora_adamw_state_values"):
         getattr(L, name).restype = c_i32
     _lib = L
     return L
@@ -728,6 +746,140 @@ def qlora_layer_norm_bwd(dY: torch.Tensor, S: torch.Tensor, weight: torch.Tensor
     _check(lib().qlora_layer_norm_bwd(ctypes.byref(n), pdY, pS, pw, pm, pr, pdS, pdX, pdw, pdb, workspace.data_ptr(),
                                       _nbytes(workspace), raw))
     return dX, dweight, dbias
+
+
+ADAMW_BLOCK = 256       # values that share one scale of an 8-bit state
+
+
+@dataclass
+class AdamWState:
+    """The tensors of qlora_adamw_step and their moments.  The moments of all
+    tensors lie in flat buffers, each tensor's from a multiple of 256 values on
+    (`starts`): m and v fp32, or m E4M3 and v uint8 codes with one fp32 scale per
+    block of 256.  All zeros is the state before the first step.  The addresses
+    of `params`, `grads` and `copies` are read once: the tensors have to stay
+    where they are (use `set_grads` for other gradient tensors)."""
+    params: list
+    grads: list
+    copies: Optional[list]
+    state_bits: int
+    starts: list
+    m: torch.Tensor
+    v: torch.Tensor
+    m_scale: Optional[torch.Tensor]
+    v_scale: Optional[torch.Tensor]
+    array: object              # qlora_adamw_tensor_t[len(params)]
+    device: torch.device
+
+    def set_grads(self, grads) -> None:
+        """Take the gradients from these tensors from now on."""
+        grads = _adamw_tensors(grads, "grads", self.params, self.device)
+        _dt(grads[0], "grads")
+        self.grads = grads
+        for t, g in zip(self.array, grads):
+            t.grad = g.data_ptr()
+
+
+def _adamw_tensors(ts, name: str, params, dev) -> list:
+    ts = list(ts)
+    if len(ts) != len(params):
+        raise ValueError(f"{name}: {len(ts)} tensors for {len(params)} parameters")
+    for i, (t, p) in enumerate(zip(ts, params)):
+        _expect(t, f"{name}[{i}]", p.shape, ts[0].dtype)
+        if t.device != dev:
+            raise ValueError(f"{name}[{i}] is on {t.device}, the parameters on {dev}")
+    return ts
+
+
+def qlora_adamw_alloc(params, grads, state_bits: int = 32, copies=None) -> AdamWState:
+    """State for AdamW over many tensors: params (all bf16 or all fp32), their
+    gradients (all bf16 or all fp32, the same shapes) and, beside fp32 params,
+    bf16 copies that every step writes (the adapters as the linear layer reads
+    them).  state_bits: 32, or 8 for block-wise 8-bit moments."""
+    params = list(params)
+    if state_bits not in (8, 32):
+        raise ValueError(f"state_bits must be 8 or 32, got {state_bits!r}")
+    if not params:
+        raise ValueError("no parameters")
+    dev = params[0].device
+    params = _adamw_tensors(params, "params", params, dev)
+    _dt(params[0], "params")
+    grads = _adamw_tensors(grads, "grads", params, dev)
+    _dt(grads[0], "grads")
+    if copies is not None:
+        copies = _adamw_tensors(copies, "copies", params, dev)
+        if params[0].dtype != torch.float32 or copies[0].dtype != torch.bfloat16:
+            raise ValueError("copies are bf16, beside fp32 parameters")
+    spans = sorted((t.data_ptr(), t.data_ptr() + _nbytes(t)) for t in params + (copies or []) if t.numel())
+    if any(b[0] < a[1] for a, b in zip(spans, spans[1:])):
+        raise ValueError("two parameters (or copies) overlap")
+    _on_cuda(params[0], "params")
+    starts, at = [], 0
+    for p in params:
+        starts.append(at)
+        at += -(-p.numel() // ADAMW_BLOCK) * ADAMW_BLOCK
+    eight = state_bits == 8
+    m = torch.zeros(at, dtype=torch.uint8 if eight else torch.float32, device=dev)
+    v = torch.zeros_like(m)
+    ms = torch.zeros(at // ADAMW_BLOCK, dtype=torch.float32, device=dev) if eight else None
+    vs = torch.zeros_like(ms) if eight else None
+    if eight:
+        m = m.view(torch.float8_e4m3fn)
+    array = (QloraAdamWTensor * len(params))()
+    for i, (t, p, g, o) in enumerate(zip(array, params, grads, starts)):
+        t.param, t.grad, t.n = p.data_ptr(), g.data_ptr(), p.numel()
+        t.copy = copies[i].data_ptr() if copies is not None else None
+        t.m, t.v = m.data_ptr() + o * m.element_size(), v.data_ptr() + o * v.element_size()
+        if eight:
+            t.m_scale, t.v_scale = ms.data_ptr() + o // ADAMW_BLOCK * 4, vs.data_ptr() + o // ADAMW_BLOCK * 4
+    return AdamWState(params, grads, copies, state_bits, starts, m, v, ms, vs, array, dev)
+
+
+def qlora_adamw_clock(lr: float, step: int = 0, device=None) -> torch.Tensor:
+    """Learning rate (element 0) and steps taken so far (element 1) in device
+    memory, for steps that a captured graph replays."""
+    device = device or torch.device("cuda", torch.cuda.current_device())
+    return torch.tensor([float(lr), float(step), 0, 0, 0, 0, 0, 0], dtype=torch.float64, device=device)
+
+
+def qlora_adamw_step(state: AdamWState, step: Optional[int] = None, lr: Optional[float] = None, betas=(0.9, 0.999),
+                     eps: float = 1e-8, weight_decay: float = 0.0, grad_scale: Optional[torch.Tensor] = None,
+                     clock: Optional[torch.Tensor] = None, stream=None) -> None:
+    """One AdamW step, in place.  `step` counts from 1; a clock (see
+    qlora_adamw_clock) takes the place of `step` and `lr`.  grad_scale: one fp32
+    value on the device that multiplies every gradient."""
+    dev = state.device
+    if (clock is None) == (step is None or lr is None) or (clock is not None and (step is not None or lr is not None)):
+        raise ValueError("either step and lr, or a clock")
+    scale = _want(grad_scale, "grad_scale", (1,), torch.float32, dev) if grad_scale is not None else None
+    tick = _want(clock, "clock", (8,), torch.float64, dev) if clock is not None else None
+    o = QloraAdamW(_DT[state.params[0].dtype], _DT[state.grads[0].dtype], state.state_bits, float(lr or 0.0),
+                   float(betas[0]), float(betas[1]), float(eps), float(weight_decay), int(step or 0), scale, tick)
+    raw, _ = _enter(dev, stream)
+    _check(lib().qlora_adamw_step(ctypes.byref(o), state.array, len(state.params), raw))
+
+
+def qlora_adamw_state(state: AdamWState, m: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
+                      stream=None):
+    """The moments as flat fp32 tensors (m, v), laid out as state.starts says:
+    the state's own with 32 bits, the values that the codes stand for with 8."""
+    if state.state_bits == 32:
+        if m is not None or v is not None:
+            raise ValueError("32-bit moments are not copied: use the returned tensors")
+        return state.m, state.v
+    n, dev = state.m.numel(), state.device
+    pm, pv = _want(m, "m", (n,), torch.float32, dev), _want(v, "v", (n,), torch.float32, dev)
+    raw, own = _enter(dev, stream)
+    with own:
+        if m is None:
+            m = torch.empty(n, dtype=torch.float32, device=dev)
+            pm = m.data_ptr()
+        if v is None:
+            v = torch.empty(n, dtype=torch.float32, device=dev)
+            pv = v.data_ptr()
+    _check(lib().qlora_adamw_state_values(n, state.m.data_ptr(), state.m_scale.data_ptr(), state.v.data_ptr(),
+                                          state.v_scale.data_ptr(), pm, pv, raw))
+    return m, v
 
 
 def qlora_nf4_codebook():

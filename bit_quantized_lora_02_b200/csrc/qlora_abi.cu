@@ -638,6 +638,71 @@ int qlora_layer_norm_bwd(const qlora_norm_t* n, const void* dY, const void* S, c
   return check_cuda(launch_norm_bwd(a, static_cast<cudaStream_t>(stream)), "qlora_layer_norm_bwd launch");
 }
 
+int qlora_adamw_step(const qlora_adamw_t* o, const qlora_adamw_tensor_t* tensors, int64_t count,
+                     qlora_stream_t stream) {
+  static_assert(sizeof(qlora_adamw_tensor_t) == sizeof(AdamTensor), "a tensor's descriptor is copied as it is");
+  if (!o) return fail(QLORA_ERR_INVALID_ARG, "AdamW descriptor is NULL");
+  if (count < 0 || (count > 0 && !tensors)) return fail(QLORA_ERR_INVALID_ARG, "bad tensor list");
+  if (o->param_dtype < 0 || o->param_dtype > 1 || o->grad_dtype < 0 || o->grad_dtype > 1)
+    return fail(QLORA_ERR_INVALID_ARG, "param_dtype and grad_dtype must be QLORA_DT_BF16 or QLORA_DT_F32");
+  if (o->state_bits != 8 && o->state_bits != 32)
+    return fail(QLORA_ERR_UNSUPPORTED, "state_bits %d not supported (8 or 32)", o->state_bits);
+  if (!(o->beta1 >= 0.0 && o->beta1 < 1.0 && o->beta2 >= 0.0 && o->beta2 < 1.0))
+    return fail(QLORA_ERR_INVALID_ARG, "beta1 and beta2 must lie in [0, 1)");
+  if (!(o->eps >= 0.0 && o->weight_decay >= 0.0)) return fail(QLORA_ERR_INVALID_ARG, "eps and weight_decay must be >= 0");
+  int rc;
+  if (o->clock) {
+    if (!aligned(o->clock, 8)) return fail(QLORA_ERR_ALIGNMENT, "clock must be 8-byte aligned");
+  } else if (!(o->lr >= 0.0) || o->step < 1) {
+    return fail(QLORA_ERR_INVALID_ARG, "lr must be >= 0 and step >= 1");
+  }
+  if ((rc = check_ptr4(o->grad_scale, "grad_scale", false))) return rc;
+  const bool eight = o->state_bits == 8;
+  AdamArgs a{};
+  int64_t some = -1;
+  for (int64_t i = 0; i < count; ++i) {
+    const qlora_adamw_tensor_t& t = tensors[i];
+    if (t.n < 0 || t.n > (int64_t(1) << 38)) return fail(QLORA_ERR_INVALID_ARG, "tensor %lld: n=%lld", (long long)i, (long long)t.n);
+    if (t.n == 0) continue;
+    if (some < 0) {
+      some = i;
+      a.copies = t.copy != nullptr;
+    }
+    if (!t.param || !t.grad || !t.m || !t.v || (eight && (!t.m_scale || !t.v_scale)))
+      return fail(QLORA_ERR_INVALID_ARG, "tensor %lld: a NULL pointer", (long long)i);
+    if ((t.copy != nullptr) != (a.copies != 0) || (t.copy && o->param_dtype != QLORA_DT_F32))
+      return fail(QLORA_ERR_INVALID_ARG, "tensor %lld: copies go with fp32 parameters, for all tensors or none", (long long)i);
+    const size_t al = eight ? 8 : 16;
+    if (!aligned(t.param, 16) || !aligned(t.grad, 16) || !aligned(t.copy, 16) || !aligned(t.m, al) || !aligned(t.v, al) ||
+        !aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))
+      return fail(QLORA_ERR_ALIGNMENT, "tensor %lld: param, grad and copy must be 16-byte aligned, states %zu", (long long)i, al);
+  }
+  if (some < 0 && !o->clock) return ok();
+  DeviceScope scope;
+  if ((rc = scope.bind(o->clock ? static_cast<const void*>(o->clock) : tensors[some].param))) return rc;
+  a.tensors = reinterpret_cast<const AdamTensor*>(tensors);
+  a.count = count; a.param_dtype = o->param_dtype; a.grad_dtype = o->grad_dtype; a.bits = o->state_bits;
+  a.lr = o->lr; a.beta1 = o->beta1; a.beta2 = o->beta2; a.eps = o->eps; a.wd = o->weight_decay; a.step = o->step;
+  a.scale = o->grad_scale; a.clock = o->clock;
+  return check_cuda(launch_adamw(a, static_cast<cudaStream_t>(stream)), "qlora_adamw_step launch");
+}
+
+int qlora_adamw_state_values(int64_t n, const uint8_t* m, const float* m_scale, const uint8_t* v, const float* v_scale,
+                             float* m_out, float* v_out, qlora_stream_t stream) {
+  if (n < 0 || n > (int64_t(1) << 38)) return fail(QLORA_ERR_INVALID_ARG, "n=%lld", (long long)n);
+  if (n == 0) return ok();
+  int rc;
+  if (!m || !v) return fail(QLORA_ERR_INVALID_ARG, "m or v is NULL");
+  if (!aligned(m, 8) || !aligned(v, 8)) return fail(QLORA_ERR_ALIGNMENT, "m and v must be 8-byte aligned");
+  if ((rc = check_ptr4(m_scale, "m_scale", true)) || (rc = check_ptr4(v_scale, "v_scale", true)) ||
+      (rc = check_ptr16(m_out, "m_out", true)) || (rc = check_ptr16(v_out, "v_out", true)))
+    return rc;
+  DeviceScope scope;
+  if ((rc = scope.bind(m_out))) return rc;
+  return check_cuda(launch_adamw_values(n, m, m_scale, v, v_scale, m_out, v_out, static_cast<cudaStream_t>(stream)),
+                    "qlora_adamw_state_values launch");
+}
+
 int qlora_nf4_codebook(float out[16]) {
   if (!out) return fail(QLORA_ERR_INVALID_ARG, "out is NULL");
   host_codebook(out);

@@ -74,6 +74,28 @@ size_t norm_workspace_bytes(int64_t M, int64_t D, int dtype, bool dbias);
 cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t st);
 cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t st);
 
+// AdamW over many tensors (qlora_adamw.cu)
+struct AdamTensor {
+  void* p;             // parameter (bf16, or fp32)
+  uint16_t* copy;      // bf16 copy of an fp32 parameter (all tensors of a call or none)
+  const void* g;
+  int64_t n;
+  void *m, *v;         // fp32 moments, or 8-bit codes
+  float *ms, *vs;      // scales of the codes, one per block of 256
+};                     // laid out as qlora_adamw_tensor_t
+struct AdamArgs {
+  const AdamTensor* tensors;
+  int64_t count;
+  int param_dtype, grad_dtype, bits, copies;
+  double lr, beta1, beta2, eps, wd;
+  int64_t step;
+  const float* scale;  // gradient scale on the device, or nullptr
+  double* clock;       // lr and step count on the device, or nullptr
+};
+cudaError_t launch_adamw(const AdamArgs& a, cudaStream_t st);
+cudaError_t launch_adamw_values(int64_t n, const uint8_t* m8, const float* ms, const uint8_t* v8, const float* vs,
+                                float* m_out, float* v_out, cudaStream_t st);
+
 // linear layer (qlora_gemm.cu)
 struct LinearArgs {
   const uint16_t* X;    // M x k

@@ -41,8 +41,10 @@ struct Vec<float> {
   }
 };
 
-// Two fp32 values in one 64-bit register (packed f32x2 arithmetic of sm_100:
-// each half is one IEEE operation, rounded to nearest even).
+// Two fp32 values in one 64-bit register (packed f32x2 arithmetic of sm_100, each
+// half rounded to nearest even).  ptxas 12.9 contracts f2_add(f2_mul(a, b), c) to
+// one f2_fma, its .rn notwithstanding (measured): where both roundings count,
+// one of the two has to be the scalar __fmul_rn or __fadd_rn.
 using f2 = uint64_t;
 __device__ __forceinline__ f2 f2_make(float lo, float hi) {
   f2 r;

@@ -368,6 +368,63 @@ int qlora_layer_norm_bwd(const qlora_norm_t *n, const void *dY, const void *S, c
                          const float *rstd, const void *dS, void *dX, float *dweight, float *dbias, void *workspace,
                          size_t workspace_bytes, qlora_stream_t stream);
 
+/* One AdamW step over many tensors at once (Loshchilov and Hutter, "Decoupled
+ * Weight Decay Regularization", ICLR 2019), for the adapters that
+ * qlora_linear_bwd gives the gradients of:
+ *     g  = grad_scale grad
+ *     m' = beta1 m + (1 - beta1) g,   v' = beta2 v + (1 - beta2) g^2
+ *     p' = p (1 - lr wd) - lr / (1 - beta1^t) m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
+ * with the moments in 32 bits, or in 8 with one fp32 scale each for every block
+ * of 256 values of a tensor (the last may be shorter):
+ *     m: E4M3 codes of RN32(m RN32(448 / s)), s = the block's largest |m| (0 when
+ *        that is below 2^-100); a code c stands for RN32(c RN32(s RN32(1 / 448)));
+ *     v: codes round(RN32(u RN32(255 / s))), ties to even, of the fourth root
+ *        u = RN32(sqrt(RN32(sqrt(v)))), s = the block's largest u; at least 1 where
+ *        v > 0.  A code c stands for the fourth power (two RN32 squarings) of
+ *        RN32(c RN32(s RN32(1 / 255))).
+ * p' comes from m' and v' before they are coded.  On the way to a coded moment
+ * every product and sum is rounded on its own, so the states are
+ * bit-reproducible.  All-zero codes and scales are the state before the first
+ * step. */
+typedef struct {
+  void *param;      /* n values, bf16 or fp32 (16-byte aligned)                     */
+  uint16_t *copy;   /* n bf16, receives param rounded (the adapters as the linear   *
+                     * layer reads them); only beside fp32 param, for all tensors   *
+                     * of a call or for none; else NULL                             */
+  const void *grad; /* n values, bf16 or fp32 (16-byte aligned)                     */
+  int64_t n;        /* values, >= 0                                                 */
+  void *m, *v;      /* n fp32 each (16-byte aligned), or n codes each (8-byte       *
+                     * aligned)                                                     */
+  float *m_scale, *v_scale; /* ceil(n / 256) fp32 each with 8-bit states            */
+} qlora_adamw_tensor_t;
+
+typedef struct {
+  int32_t param_dtype, grad_dtype; /* QLORA_DT_*, the same for all tensors of a call */
+  int32_t state_bits;              /* 32 or 8                                        */
+  double lr, beta1, beta2, eps, weight_decay; /* 0 <= beta < 1, the others >= 0      */
+  int64_t step;                    /* t, counted from 1                              */
+  const float *grad_scale;         /* device fp32, or NULL for 1 (a clipping factor, *
+                                    * the inverse of a loss scale)                   */
+  double *clock;                   /* NULL, or 8 device doubles (8-byte aligned):    *
+                                    * [0] lr, [1] steps taken so far, [2..7]         *
+                                    * scratch.  The call adds 1 to [1] and takes lr  *
+                                    * and t from here instead of from this struct,   *
+                                    * so that a captured graph advances when it is   *
+                                    * replayed.                                      */
+} qlora_adamw_t;
+
+/* The step over `count` tensors (host array, read during the call only).
+ * Tensors must not overlap: a parameter listed twice is a race.  A non-finite
+ * gradient spoils its parameter and moments, with 8-bit states the moments of
+ * its block of 256. */
+int qlora_adamw_step(const qlora_adamw_t *o, const qlora_adamw_tensor_t *tensors, int64_t count,
+                     qlora_stream_t stream);
+
+/* The values that n coded moments stand for (blocks of 256 from the first
+ * value on): m_out and v_out receive n fp32 each (16-byte aligned). */
+int qlora_adamw_state_values(int64_t n, const uint8_t *m, const float *m_scale, const uint8_t *v,
+                             const float *v_scale, float *m_out, float *v_out, qlora_stream_t stream);
+
 /* The library's NF4 table C[0..15] (fp32, ascending) copied to host memory. */
 int qlora_nf4_codebook(float out[16]);
 

@@ -96,3 +96,83 @@ def test_norm_oracle_gradient():
                 args = [x, w, b]
                 num = (f(*(hi if j == k else a for j, a in enumerate(args))) - f(*(lo if j == k else a for j, a in enumerate(args)))) / 2e-5
                 assert abs(num - g) < 1e-7
+
+
+# ---------------------------------------------------------------------------
+# AdamW
+# ---------------------------------------------------------------------------
+def test_adamw_refusals_of_the_binding():
+    p, g = [torch.zeros(4, 8), torch.zeros(3)], [torch.zeros(4, 8), torch.zeros(3)]
+    for args, kw, match in (((p, g), {}, "must be on a CUDA device"), ((p, g[:1]), {}, "1 tensors for 2"),
+                            ((p, [g[0], torch.zeros(4)]), {}, "grads\\[1\\]: shape"),
+                            ((p, [g[0], torch.zeros(3, dtype=BF16)]), {}, "grads\\[1\\]: dtype"),
+                            (([], []), {}, "no parameters"), ((p, g), dict(state_bits=16), "state_bits"),
+                            ((p, g), dict(copies=p), "copies are bf16"),
+                            (([p[0], p[0]], [g[0], g[0]]), {}, "overlap"),
+                            (([torch.zeros(8, 4).t()], [torch.zeros(4, 8)]), {}, "contiguous"),
+                            (([torch.zeros(3, dtype=torch.float16)], [torch.zeros(3)]), {}, "params: dtype")):
+        with pytest.raises(ValueError, match=match):
+            Q.qlora_adamw_alloc(*args, **kw)
+    flat = torch.zeros(64)
+    with pytest.raises(ValueError, match="overlap"):
+        Q.qlora_adamw_alloc([flat[:40], flat[32:]], [torch.zeros(40), torch.zeros(32)])
+
+
+def test_adamw_refusals_of_the_library(L):
+    def opt(pd=1, gd=1, bits=32, lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, wd=0.0, step=1, scale=None, clock=None):
+        return ctypes.byref(Q.QloraAdamW(pd, gd, bits, lr, b1, b2, eps, wd, step, scale, clock))
+
+    def one(param=0x1000, copy=None, grad=0x2000, n=100, m=0x3000, v=0x4000, ms=None, vs=None):
+        return (Q.QloraAdamWTensor * 1)(Q.QloraAdamWTensor(param, copy, grad, n, m, v, ms, vs))
+    step = L.qlora_adamw_step
+    assert step(None, one(), 1, None) == -1
+    assert step(opt(), None, 1, None) == -1 and step(opt(), one(), -1, None) == -1
+    assert step(opt(), None, 0, None) == 0 and step(opt(), one(n=0), 1, None) == 0     # nothing to do
+    assert step(opt(pd=2), one(), 1, None) == -1 and step(opt(gd=-1), one(), 1, None) == -1
+    assert step(opt(bits=16), one(), 1, None) == -2
+    for kw in (dict(b1=1.0), dict(b1=-0.1), dict(b2=float("nan")), dict(eps=-1.0), dict(wd=-1.0), dict(lr=float("nan")),
+               dict(lr=-1.0), dict(step=0)):
+        assert step(opt(**kw), one(), 1, None) == -1, kw
+    assert step(opt(clock=0x1004), one(), 1, None) == -3 and step(opt(scale=0x1002), one(), 1, None) == -3
+    for kw in (dict(param=None), dict(grad=None), dict(m=None), dict(v=None), dict(n=-1)):
+        assert step(opt(), one(**kw), 1, None) == -1, kw
+    assert step(opt(bits=8), one(), 1, None) == -1                                     # no scales
+    assert step(opt(pd=0), one(copy=0x5000), 1, None) == -1                            # a copy beside bf16
+    for kw in (dict(param=0x1008), dict(grad=0x2004), dict(m=0x3008), dict(copy=0x5008)):
+        assert step(opt(), one(**kw), 1, None) == -3, kw
+    two = (Q.QloraAdamWTensor * 2)(one()[0], one(copy=0x5000)[0])
+    assert step(opt(), two, 2, None) == -1                                             # copies for all or none
+    vals = L.qlora_adamw_state_values
+    assert vals(0, None, None, None, None, None, None, None) == 0 and vals(-1, None, None, None, None, None, None, None) == -1
+    assert vals(10, None, 0x1000, 0x1000, 0x1000, 0x1000, 0x1000, None) == -1
+    assert vals(10, 0x1004, 0x1000, 0x1000, 0x1000, 0x1000, 0x1000, None) == -3
+    assert vals(10, 0x1000, 0x1000, 0x1000, 0x1000, 0x1008, 0x1000, None) == -3
+
+
+def test_adamw_oracle_codes():
+    """E4M3 codes against torch's conversion for every code, every midpoint and
+    random values; coded states against their own error bounds (half a step: 2^-4
+    of m above the subnormals, half a code of the fourth root)."""
+    vals = SO.e4m3_values()
+    t = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).float().numpy()
+    assert np.array_equal(np.isnan(vals), np.isnan(t)) and np.array_equal(vals[~np.isnan(vals)], t[~np.isnan(t)])
+    pos = np.sort(vals[:127])
+    y = np.concatenate([pos, (pos[1:] + pos[:-1]) / 2, np.random.default_rng(0).uniform(-448, 448, 1000)]).astype(np.float32)
+    y = np.concatenate([y, -y])
+    assert np.array_equal(SO.e4m3_code(y), torch.from_numpy(y).to(torch.float8_e4m3fn).view(torch.uint8).numpy())
+    rng = np.random.default_rng(1)
+    m, v = rng.normal(size=1000).astype(np.float32), (rng.normal(size=1000) ** 2).astype(np.float32)
+    mc, ms, vc, vs = SO.adamw_encode(m, v)
+    dm, dv = SO.adamw_decode(mc, ms, vc, vs)
+    j = np.arange(1000) // 256
+    assert ms.shape == (4,) and np.all(np.abs(dm - m) <= np.maximum(2.0 ** -4 * np.abs(m), ms[j] / 448 * 2.0 ** -10) * 1.0001)
+    root, got = v.astype(np.float64) ** 0.25, dv.astype(np.float64) ** 0.25
+    assert np.all(np.abs(got - root) <= vs[j] / 255 * 0.5001 + 1e-6)
+    assert np.all(vc[v > 0] >= 1)
+
+
+def test_adamw_oracle_step():
+    """The plain step against a hand-worked value: p = 1, g = 0.5, first step: m' =
+    0.05, v' = 0.00025, both corrected to 0.5 and 0.25, so the update is lr."""
+    p, m, v = SO.adamw_param(np.array([1.0]), np.zeros(1), np.zeros(1), np.array([0.5]), 1, 0.1, 0.9, 0.999, 0.0, 0.2)
+    assert np.allclose(p, 1.0 * (1 - 0.02) - 0.1) and np.allclose(m, 0.05) and np.allclose(v, 0.00025)
