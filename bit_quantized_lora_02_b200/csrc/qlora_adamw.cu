@@ -25,11 +25,14 @@
 //
 // Bound: HBM.  bf16 parameters with fp32 gradients and 8-bit states move 12 bytes
 // per value, fp32 masters with bf16 copies and 32-bit states 30.  A warp holds one
-// block of 256 values, 8 to a lane; the block's maxima are one redux each.
+// block of 256 values, 8 to a lane, with the loads of the next ones in flight
+// (cp.async: registers cannot hold them as well); the block's maxima are one redux
+// each.
 // Tensors, their pointers and the chunk where each starts travel as kernel
 // parameters (up to 28 KB): nothing has to be copied to the device before the
 // launch, and a captured graph keeps them.
 #include <cmath>
+#include <type_traits>
 
 #include "qlora_device.cuh"
 #include "qlora_internal.h"
@@ -40,6 +43,14 @@ namespace qlora {
 namespace {
 
 constexpr int kBlock = 256;
+constexpr int kWarps = 4;               // warps of a CTA, one block each at a time
+// Blocks that a warp's loads run ahead.  128M values: with 8-bit states, whose
+// arithmetic takes long, 242 us at three; with 32-bit ones one is enough (564 us
+// with fp32 parameters; two and three were 15% slower at some combinations of
+// types, where their rings fill an SM's shared memory).
+template <bool EIGHT>
+constexpr int kAheadBlocks = EIGHT ? 3 : 1;
+constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23
 
 struct Scalars {
   float b1, c1, b2, c2;      // beta, 1 - beta
@@ -71,104 +82,327 @@ __global__ void k_adamw_clock(double* clock, double beta1, double beta2, double 
   out[2] = static_cast<float>(1.0 / sqrt(1.0 - pow(beta2, t)));
 }
 
-// 8 values of a lane, at element i of an array of n; `have` of them exist.  At the
+// Four neighbouring elements of 4, 2 or 1 bytes: one load or store per lane, a
+// warp's together contiguous.  `have` of the four exist (the array has n); at the
 // array's end every load's address is clamped into it.
-template <typename T>
-__device__ __forceinline__ void load8(const void* base, int64_t i, int64_t n, int have, float (&f)[8]) {
-  const T* p = reinterpret_cast<const T*>(base) + i;
-  if (have == 8) {
-    constexpr int N = Vec<T>::N;
-    uint4 q[8 / N];
+template <typename E>
+struct Four;
+template <>
+struct Four<float> {
+  using Raw = uint4;
+};
+template <>
+struct Four<__nv_bfloat16> {
+  using Raw = uint2;
+};
+template <>
+struct Four<uint8_t> {
+  using Raw = uint32_t;
+};
+template <typename E>
+__device__ __forceinline__ uint32_t bits_of(E x) {
+  if constexpr (sizeof(E) == 4)
+    return __float_as_uint(x);
+  else if constexpr (sizeof(E) == 2)
+    return __bfloat16_as_ushort(x);
+  else
+    return x;
+}
+template <typename E>
+__device__ __forceinline__ typename Four<E>::Raw load4(const void* base, int64_t i, int64_t n, int have) {
+  const E* p = reinterpret_cast<const E*>(base);
+  if (have == 4) return *reinterpret_cast<const typename Four<E>::Raw*>(p + i);
+  uint32_t x[4];
 #pragma unroll
-    for (int h = 0; h < 8 / N; ++h) q[h] = reinterpret_cast<const uint4*>(p)[h];
-#pragma unroll
-    for (int h = 0; h < 8 / N; ++h) {
-      float x[N];
-      Vec<T>::unpack(q[h], x);
-#pragma unroll
-      for (int k = 0; k < N; ++k) f[h * N + k] = x[k];
-    }
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t b = bits_of(p[min(i + k, n - 1)]);
+    x[k] = k < have ? b : 0u;
+  }
+  if constexpr (sizeof(E) == 4)
+    return make_uint4(x[0], x[1], x[2], x[3]);
+  else if constexpr (sizeof(E) == 2)
+    return make_uint2(x[0] | x[1] << 16, x[2] | x[3] << 16);
+  else
+    return x[0] | x[1] << 8 | x[2] << 16 | x[3] << 24;
+}
+template <typename E>
+__device__ __forceinline__ void store4(void* base, int64_t i, int have, const typename Four<E>::Raw& v) {
+  E* p = reinterpret_cast<E*>(base) + i;
+  if (have == 4) {
+    *reinterpret_cast<typename Four<E>::Raw*>(p) = v;
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float x = to_f32(reinterpret_cast<const T*>(base)[min(i + k, n - 1)]);
-      f[k] = k < have ? x : 0.0f;
+    for (int k = 0; k < 4; ++k) {
+      if (k >= have) continue;
+      if constexpr (sizeof(E) == 4)
+        p[k] = __uint_as_float(k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w);
+      else if constexpr (sizeof(E) == 2)
+        p[k] = __ushort_as_bfloat16(static_cast<unsigned short>((k < 2 ? v.x : v.y) >> (16 * (k & 1))));
+      else
+        p[k] = static_cast<uint8_t>(v >> (8 * k));
     }
   }
 }
-
-template <typename T>
-__device__ __forceinline__ void store8(void* base, int64_t i, int have, const float (&f)[8]) {
-  T* p = reinterpret_cast<T*>(base) + i;
-  if (have == 8) {
-    constexpr int N = Vec<T>::N;
-#pragma unroll
-    for (int h = 0; h < 8 / N; ++h) {
-      float x[N];
-#pragma unroll
-      for (int k = 0; k < N; ++k) x[k] = f[h * N + k];
-      reinterpret_cast<uint4*>(p)[h] = Vec<T>::pack(x);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < have) p[k] = from_f32<T>(f[k]);
-  }
+__device__ __forceinline__ void pairs(const uint4& v, f2 (&f)[2]) {
+  f[0] = f2_make(__uint_as_float(v.x), __uint_as_float(v.y));
+  f[1] = f2_make(__uint_as_float(v.z), __uint_as_float(v.w));
 }
-
-// 8 byte codes, the first in the low byte of x
-__device__ __forceinline__ uint2 load8b(const void* base, int64_t i, int64_t n, int have) {
-  const uint8_t* p = reinterpret_cast<const uint8_t*>(base);
-  if (have == 8) return *reinterpret_cast<const uint2*>(p + i);
-  uint2 v = make_uint2(0u, 0u);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t x = p[min(i + k, n - 1)];
-    const uint32_t b = k < have ? x << (8 * (k & 3)) : 0u;
-    if (k < 4)
-      v.x |= b;
-    else
-      v.y |= b;
-  }
-  return v;
+__device__ __forceinline__ void pairs(const uint2& v, f2 (&f)[2]) {
+  f[0] = f2_make(bf16_lo(v.x), bf16_hi(v.x));
+  f[1] = f2_make(bf16_lo(v.y), bf16_hi(v.y));
 }
-__device__ __forceinline__ void store8b(void* base, int64_t i, int have, uint2 v) {
-  uint8_t* p = reinterpret_cast<uint8_t*>(base) + i;
-  if (have == 8) {
-    *reinterpret_cast<uint2*>(p) = v;
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < have) p[k] = static_cast<uint8_t>((k < 4 ? v.x : v.y) >> (8 * (k & 3)));
-  }
-}
+__device__ __forceinline__ uint4 raw_f32(const f2 (&f)[2]) { return pack2(f, 0.0f); }
+__device__ __forceinline__ uint2 raw_bf16(const f2 (&f)[2]) { return make_uint2(pack2_bf16(f[0]), pack2_bf16(f[1])); }
 
-// m and v of 8 codes each (scales: the block's largest |m|, largest fourth root)
-__device__ __forceinline__ void decode(uint2 mc, uint2 vc, float ms, float vs, float (&m)[8], float (&v)[8]) {
-  const f2 dm = f2_dup(__fmul_rn(ms, 1.0f / 448.0f)), dv = f2_dup(__fmul_rn(vs, 1.0f / 255.0f));
+// m and v of four codes each (dm, dv: the block's scales over 448 and 255)
+__device__ __forceinline__ void decode(uint32_t mc, uint32_t vc, f2 dm, f2 dv, f2 (&m)[2], f2 (&v)[2]) {
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    const uint32_t mw = h < 2 ? mc.x : mc.y, vw = h < 2 ? vc.x : vc.y;
+  for (int h = 0; h < 2; ++h) {
     uint32_t half2;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(half2) : "h"(static_cast<uint16_t>(mw >> (16 * (h & 1)))));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(half2) : "h"(static_cast<uint16_t>(mc >> (16 * h))));
     float lo, hi;
     asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
         : "=f"(lo), "=f"(hi)
         : "r"(half2));
-    f2_get(f2_mul(f2_make(lo, hi), dm), m[2 * h], m[2 * h + 1]);
+    m[h] = f2_mul(f2_make(lo, hi), dm);
     // a byte b as 2^23 + b, so that one exact subtraction gives the float
-    const float a = __uint_as_float(prmt(vw, 0x4B000000u, (h & 1) ? 0x7442u : 0x7440u)) - 8388608.0f;
-    const float b = __uint_as_float(prmt(vw, 0x4B000000u, (h & 1) ? 0x7443u : 0x7441u)) - 8388608.0f;
-    f2 t = f2_mul(f2_make(a, b), dv);
+    const float a = __uint_as_float(prmt(vc, 0x4B000000u, h ? 0x7442u : 0x7440u));
+    const float b = __uint_as_float(prmt(vc, 0x4B000000u, h ? 0x7443u : 0x7441u));
+    f2 t = f2_mul(f2_add(f2_make(a, b), f2_dup(-8388608.0f)), dv);
     t = f2_mul(t, t);
-    f2_get(f2_mul(t, t), v[2 * h], v[2 * h + 1]);
+    v[h] = f2_mul(t, t);
   }
+}
+__device__ __forceinline__ float unit_m(float s) { return __fmul_rn(s, 1.0f / 448.0f); }
+__device__ __forceinline__ float unit_v(float s) { return __fmul_rn(s, 1.0f / 255.0f); }
+
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float sqrt_approx_ftz(float x) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// largest of a and two magnitudes, NaN if one is
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+  return r;
 }
 
 enum { kParamBf16 = 0, kParamF32 = 1, kParamMaster = 2 };   // master: fp32 and a bf16 copy
 
+// One block of 256 values, 8 to a lane: elements 4 lane + k and 128 + 4 lane + k.
+template <int PARAM, typename G, bool EIGHT>
+struct Block {
+  using P = typename std::conditional<PARAM == kParamBf16, __nv_bfloat16, float>::type;
+  using S = typename std::conditional<EIGHT, uint8_t, float>::type;
+  typename Four<G>::Raw g[2];
+  typename Four<P>::Raw p[2];
+  typename Four<S>::Raw m[2], v[2];
+  uint2 copy[2];
+  float ms, vs;
+
+  // the moments, the parameter and, in 8 bits, the codes after the step
+  __device__ __forceinline__ void step(const Scalars& s, f2 gs) {
+    const f2 b1 = f2_dup(s.b1), c1 = f2_dup(s.c1), b2 = f2_dup(s.b2), c2 = f2_dup(s.c2);
+    const f2 decay = f2_dup(s.decay), size = f2_dup(-s.size), rbc2 = f2_dup(s.rbc2), eps = f2_dup(s.eps);
+    f2 mn[4], vn[4], root[4];
+    float mtop = 0.0f, vtop = 0.0f;
+    f2 dm = 0, dv = 0;
+    if constexpr (EIGHT) {
+      dm = f2_dup(unit_m(ms));
+      dv = f2_dup(unit_v(vs));
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      f2 gr[2], pa[2], mo[2], vo[2];
+      pairs(g[j], gr);
+      pairs(p[j], pa);
+      if constexpr (EIGHT) {
+        decode(m[j], v[j], dm, dv, mo, vo);
+      } else {
+        pairs(m[j], mo);
+        pairs(v[j], vo);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int q = 2 * j + h;
+        gr[h] = f2_mul(gr[h], gs);
+        // packed products, but scalar sums: the compiler fuses a packed product
+        // into the packed sum behind it, which would round once instead of twice
+        float a0, a1, q0, q1, x0, x1;
+        f2_get(f2_mul(mo[h], b1), a0, a1);
+        f2_get(f2_mul(gr[h], c1), q0, q1);
+        x0 = __fadd_rn(a0, q0);
+        x1 = __fadd_rn(a1, q1);
+        if constexpr (EIGHT) mtop = max3_nan(mtop, x0, x1);
+        mn[q] = f2_make(x0, x1);
+        f2_get(f2_mul(vo[h], b2), a0, a1);
+        f2_get(f2_mul(f2_mul(gr[h], gr[h]), c2), q0, q1);
+        x0 = __fadd_rn(a0, q0);
+        x1 = __fadd_rn(a1, q1);
+        if constexpr (EIGHT) vtop = max3_nan(vtop, x0, x1);
+        vn[q] = f2_make(x0, x1);
+        root[q] = f2_make(sqrt_approx(x0), sqrt_approx(x1));
+        // p (1 - lr wd) + m' (-lr / (1 - beta1^t)) / (sqrt(v') / sqrt(1 - beta2^t) + eps)
+        f2_get(f2_fma(root[q], rbc2, eps), a0, a1);
+        pa[h] = f2_fma(pa[h], decay, f2_mul(f2_mul(mn[q], size), f2_make(rcp_approx(a0), rcp_approx(a1))));
+      }
+      if constexpr (PARAM == kParamBf16) {
+        p[j] = raw_bf16(pa);
+      } else {
+        p[j] = raw_f32(pa);
+        if constexpr (PARAM == kParamMaster) copy[j] = raw_bf16(pa);
+      }
+      if constexpr (!EIGHT) {
+        m[j] = raw_f32({mn[2 * j], mn[2 * j + 1]});
+        v[j] = raw_f32({vn[2 * j], vn[2 * j + 1]});
+      }
+    }
+    if constexpr (EIGHT) {
+      // magnitudes order as integers, NaN above infinity
+      ms = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mtop) & 0x7FFFFFFFu));
+      const float vmax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(vtop) & 0x7FFFFFFFu));
+      // rounded square roots keep the order, so the largest root is the root of the largest
+      vs = __fsqrt_rn(__fsqrt_rn(vmax));
+      if (ms < 0x1p-100f) ms = 0.0f;
+      const float im = ms > 0.0f ? __fdiv_rn(448.0f, ms) : 0.0f;
+      const float iv = vs > 0.0f ? __fdiv_rn(255.0f, vs) : 0.0f;
+      const f2 im2 = f2_dup(im), iv2 = f2_dup(iv), unmagic = f2_dup(-kMagic), minus = f2_dup(-1.0f);
+      // y = u 255 / s_u from approximate roots first: they are off by at most 2^-23
+      // of their value each, and the definition's y by roundings of its own, 6.5 *
+      // 2^-24 in all or 1e-4 of y <= 255.  Where y is not within 2^-13 of a half
+      // between two codes, both give the same code.
+      f2 t[4];
+      float worst = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float x0, x1;
+        f2_get(root[q], x0, x1);
+        const f2 y = f2_mul(f2_make(sqrt_approx_ftz(x0), sqrt_approx_ftz(x1)), iv2);
+        f2_get(y, x0, x1);
+        // adding 1.5 * 2^23 rounds to an integer (ties to even) in the low byte
+        t[q] = f2_make(__fadd_rn(x0, kMagic), __fadd_rn(x1, kMagic));
+        f2_get(f2_fma(f2_add(t[q], unmagic), minus, y), x0, x1);
+        worst = fmaxf(fmaxf(fabsf(x0), fabsf(x1)), worst);
+      }
+      if (worst > 0.5f - 0x1p-13f) {   // one block in fifteen: the roots as the definition has them
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float x0, x1;
+          f2_get(vn[q], x0, x1);
+          x0 = __fmul_rn(__fsqrt_rn(__fsqrt_rn(x0)), iv);
+          x1 = __fmul_rn(__fsqrt_rn(__fsqrt_rn(x1)), iv);
+          t[q] = f2_make(__fadd_rn(x0, kMagic), __fadd_rn(x1, kMagic));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint16_t e[2];
+        float c[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float x0, x1;
+          f2_get(f2_mul(mn[2 * j + h], im2), x0, x1);
+          asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e[h]) : "f"(x1), "f"(x0));
+          f2_get(t[2 * j + h], c[2 * h], c[2 * h + 1]);
+          f2_get(vn[2 * j + h], x0, x1);
+          if (x0 > 0.0f) c[2 * h] = fmaxf(c[2 * h], kMagic + 1.0f);
+          if (x1 > 0.0f) c[2 * h + 1] = fmaxf(c[2 * h + 1], kMagic + 1.0f);
+        }
+        m[j] = static_cast<uint32_t>(e[0]) | (static_cast<uint32_t>(e[1]) << 16);
+        v[j] = prmt(prmt(__float_as_uint(c[0]), __float_as_uint(c[1]), 0x0040u),
+                    prmt(__float_as_uint(c[2]), __float_as_uint(c[3]), 0x0040u), 0x5410u);
+      }
+    }
+  }
+};
+
+// The lane's place in the arrays of a tensor, and steps of kWarps blocks.
+template <int PARAM, typename G, bool EIGHT>
+struct Place {
+  using B = Block<PARAM, G, EIGHT>;
+  const uint8_t* g;
+  uint8_t *p, *m, *v, *copy;
+  template <typename E>
+  static __device__ __forceinline__ uint8_t* at(const void* base, int64_t i) {
+    return const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(base)) + i * static_cast<int64_t>(sizeof(E));
+  }
+  __device__ __forceinline__ Place(const AdamTensor& T, int64_t block, int lane) {
+    const int64_t i = block * kBlock + 4 * lane;
+    g = at<G>(T.g, i);
+    p = at<typename B::P>(T.p, i);
+    m = at<typename B::S>(T.m, i);
+    v = at<typename B::S>(T.v, i);
+    copy = PARAM == kParamMaster ? at<uint16_t>(T.copy, i) : p;
+  }
+  __device__ __forceinline__ void advance() {
+    constexpr int E = kWarps * kBlock;
+    g += E * sizeof(G);
+    p += E * sizeof(typename B::P);
+    m += E * sizeof(typename B::S);
+    v += E * sizeof(typename B::S);
+    if constexpr (PARAM == kParamMaster) copy += E * 2;
+  }
+  template <typename E>
+  static __device__ __forceinline__ void put(uint8_t* q, int j, const typename Four<E>::Raw& x) {
+    *reinterpret_cast<typename Four<E>::Raw*>(q + j * 128 * sizeof(E)) = x;
+  }
+  // A block's loads run ahead through a ring in shared memory (cp.async); a lane
+  // reads back only what it copied itself.  Every array has two slots of four
+  // elements per thread and stage.
+  static constexpr uint32_t kT = 32 * kWarps;
+  static constexpr uint32_t kG = 0, kP = kG + 8 * kT * sizeof(G), kM = kP + 8 * kT * sizeof(typename B::P),
+                            kV = kM + 8 * kT * sizeof(typename B::S), kStage = kV + 8 * kT * sizeof(typename B::S);
+  template <typename E>
+  static __device__ __forceinline__ void copy_in(uint32_t ring, const uint8_t* q) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      cp_async<4 * sizeof(E)>(ring + (j * kT + threadIdx.x) * 4 * sizeof(E), q + j * 128 * sizeof(E));
+  }
+  __device__ __forceinline__ void issue(uint32_t stage) const {
+    copy_in<G>(stage + kG, g);
+    copy_in<typename B::P>(stage + kP, p);
+    copy_in<typename B::S>(stage + kM, m);
+    copy_in<typename B::S>(stage + kV, v);
+  }
+  template <typename E>
+  static __device__ __forceinline__ typename Four<E>::Raw take(uint32_t ring, int j) {
+    return lds<typename Four<E>::Raw>(ring + (j * kT + threadIdx.x) * 4 * sizeof(E));
+  }
+  static __device__ __forceinline__ void load(B& b, uint32_t stage) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      b.g[j] = take<G>(stage + kG, j);
+      b.p[j] = take<typename B::P>(stage + kP, j);
+      b.m[j] = take<typename B::S>(stage + kM, j);
+      b.v[j] = take<typename B::S>(stage + kV, j);
+    }
+  }
+  __device__ __forceinline__ void store(const B& b) const {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      put<typename B::P>(p, j, b.p[j]);
+      if constexpr (PARAM == kParamMaster) put<__nv_bfloat16>(copy, j, b.copy[j]);
+      put<typename B::S>(m, j, b.m[j]);
+      put<typename B::S>(v, j, b.v[j]);
+    }
+  }
+};
+
 template <int PARAM, typename G, bool EIGHT, int CAP>
-__global__ void __launch_bounds__(256) k_adamw(const __grid_constant__ Batch<CAP> b) {
+__global__ void __launch_bounds__(32 * kWarps, 5) k_adamw(const __grid_constant__ Batch<CAP> b) {
+  using B = Block<PARAM, G, EIGHT>;
+  constexpr int kAhead = kAheadBlocks<EIGHT>;
   griddep_launch_dependents();
   // the tensor whose chunks hold this CTA's
   int lo = 0, hi = b.count - 1;
@@ -183,6 +417,11 @@ __global__ void __launch_bounds__(256) k_adamw(const __grid_constant__ Batch<CAP
   const AdamTensor& T = b.t[lo];
   const int64_t n = T.n;
   const int lane = threadIdx.x & 31;
+  const int64_t block = static_cast<int64_t>(chunk - b.first[lo]) * kWarps * b.iters + (threadIdx.x >> 5);
+  // this warp's blocks: `whole` of 256 values, kWarps apart, and maybe the tensor's
+  // shorter last one
+  const int64_t full = n / kBlock;
+  const int whole = static_cast<int>(min(max((full - block + kWarps - 1) / kWarps, int64_t(0)), static_cast<int64_t>(b.iters)));
   griddep_wait();
   Scalars s = b.s;
   if (b.has_clock) {
@@ -190,110 +429,116 @@ __global__ void __launch_bounds__(256) k_adamw(const __grid_constant__ Batch<CAP
     s.size = b.clock[1];
     s.rbc2 = b.clock[2];
   }
-  const float gs = b.has_scale ? *b.scale : 1.0f;
-  const f2 gs2 = f2_dup(gs), b1 = f2_dup(s.b1), c1 = f2_dup(s.c1), b2 = f2_dup(s.b2), c2 = f2_dup(s.c2);
-  int64_t block = static_cast<int64_t>(chunk - b.first[lo]) * 8 * b.iters + (threadIdx.x >> 5);
-  for (int it = 0; it < b.iters; ++it, block += 8) {
-    const int64_t i = block * kBlock + lane * 8;
-    if (block * kBlock >= n) break;
-    const int have = static_cast<int>(min(max(n - i, int64_t(0)), int64_t(8)));
-    float p[8], g[8], m[8], v[8], r[8];
-    load8<G>(T.g, i, n, have, g);
-    if constexpr (PARAM == kParamBf16)
-      load8<__nv_bfloat16>(T.p, i, n, have, p);
-    else
-      load8<float>(T.p, i, n, have, p);
+  const f2 gs = f2_dup(b.has_scale ? *b.scale : 1.0f);
+  if (whole > 0) {
+    using At = Place<PARAM, G, EIGHT>;
+    extern __shared__ __align__(16) uint8_t ring_mem[];
+    const uint32_t ring = smem_u32(ring_mem);
+    At ahead(T, block, lane), at = ahead;
+    for (int k = 0; k < kAhead; ++k) {
+      if (k < whole) {
+        ahead.issue(ring + k * At::kStage);
+        ahead.advance();
+      }
+      cp_async_commit();
+    }
+    // lane k holds the scales of the warp's block k, old ones and then new ones
+    float ms = 0.0f, vs = 0.0f;
+    const int64_t mine = block + kWarps * min(lane, whole - 1);
     if constexpr (EIGHT) {
-      const uint2 mc = load8b(T.m, i, n, have), vc = load8b(T.v, i, n, have);
-      decode(mc, vc, T.ms[block], T.vs[block], m, v);
-    } else {
-      load8<float>(T.m, i, n, have, m);
-      load8<float>(T.v, i, n, have, v);
+      ms = T.ms[mine];
+      vs = T.vs[mine];
     }
+    uint32_t stage = 0;
+#pragma unroll 1
+    for (int k = 0; k < whole; ++k) {
+      B now;
+      cp_async_wait(kAhead - 1);
+      At::load(now, ring + stage);
+      if constexpr (EIGHT) {
+        now.ms = __shfl_sync(0xFFFFFFFFu, ms, k);
+        now.vs = __shfl_sync(0xFFFFFFFFu, vs, k);
+      }
+      now.step(s, gs);
+      at.store(now);
+      at.advance();
+      if constexpr (EIGHT) {
+        ms = lane == k ? now.ms : ms;
+        vs = lane == k ? now.vs : vs;
+      }
+      if (k + kAhead < whole) {
+        ahead.issue(ring + stage);
+        ahead.advance();
+      }
+      cp_async_commit();
+      stage = stage == (kAhead - 1) * At::kStage ? 0 : stage + At::kStage;
+    }
+    if (EIGHT && lane < whole) {
+      T.ms[mine] = ms;
+      T.vs[mine] = vs;
+    }
+  }
+  const int64_t last = block + kWarps * whole;
+  if (whole < b.iters && last == full && full * kBlock < n) {
+    B now;
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      f2 q = f2_make(g[2 * h], g[2 * h + 1]);
-      if (b.has_scale) q = f2_mul(q, gs2);
-      // packed products, but scalar sums: the compiler fuses a packed product
-      // into the packed sum behind it, which would round once instead of twice
-      float a0, a1, q0, q1;
-      f2_get(f2_mul(f2_make(m[2 * h], m[2 * h + 1]), b1), a0, a1);
-      f2_get(f2_mul(q, c1), q0, q1);
-      m[2 * h] = __fadd_rn(a0, q0);
-      m[2 * h + 1] = __fadd_rn(a1, q1);
-      f2_get(f2_mul(f2_make(v[2 * h], v[2 * h + 1]), b2), a0, a1);
-      f2_get(f2_mul(f2_mul(q, q), c2), q0, q1);
-      v[2 * h] = __fadd_rn(a0, q0);
-      v[2 * h + 1] = __fadd_rn(a1, q1);
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      r[k] = __fsqrt_rn(v[k]);
-      p[k] = p[k] * s.decay - __fdividef(m[k] * s.size, fmaf(r[k], s.rbc2, s.eps));
-    }
-    if constexpr (PARAM == kParamBf16) {
-      store8<__nv_bfloat16>(T.p, i, have, p);
-    } else {
-      store8<float>(T.p, i, have, p);
-      if constexpr (PARAM == kParamMaster) store8<__nv_bfloat16>(T.copy, i, have, p);
+    for (int j = 0; j < 2; ++j) {
+      const int64_t i = last * kBlock + 128 * j + 4 * lane;
+      const int have = static_cast<int>(min(max(n - i, int64_t(0)), int64_t(4)));
+      now.g[j] = load4<G>(T.g, i, n, have);
+      now.p[j] = load4<typename B::P>(T.p, i, n, have);
+      now.m[j] = load4<typename B::S>(T.m, i, n, have);
+      now.v[j] = load4<typename B::S>(T.v, i, n, have);
     }
     if constexpr (EIGHT) {
-      uint32_t mm = 0, um = 0;
+      now.ms = T.ms[last];
+      now.vs = T.vs[last];
+    }
+    now.step(s, gs);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        r[k] = __fsqrt_rn(r[k]);
-        mm = max(mm, __float_as_uint(m[k]) & 0x7FFFFFFFu);   // magnitudes order as integers (NaN above infinity)
-        um = max(um, __float_as_uint(r[k]) & 0x7FFFFFFFu);
-      }
-      float ms = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, mm));
-      const float vs = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, um));
-      if (ms < 0x1p-100f) ms = 0.0f;
-      const float im = ms > 0.0f ? __fdiv_rn(448.0f, ms) : 0.0f;
-      const float iv = vs > 0.0f ? __fdiv_rn(255.0f, vs) : 0.0f;
-      uint32_t mw[2], vw[2];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint16_t e[2];
-        uint32_t c[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          // adding 1.5 * 2^23 rounds to an integer (ties to even) in the low byte
-          const float y = __fadd_rn(__fmul_rn(r[4 * q + k], iv), 12582912.0f);
-          c[k] = max(__float_as_uint(y) & 0xFFu, v[4 * q + k] > 0.0f ? 1u : 0u);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-              : "=h"(e[k])
-              : "f"(__fmul_rn(m[4 * q + 2 * k + 1], im)), "f"(__fmul_rn(m[4 * q + 2 * k], im)));
-        mw[q] = static_cast<uint32_t>(e[0]) | (static_cast<uint32_t>(e[1]) << 16);
-        vw[q] = prmt(prmt(c[0], c[1], 0x0040u), prmt(c[2], c[3], 0x0040u), 0x5410u);
-      }
-      store8b(T.m, i, have, make_uint2(mw[0], mw[1]));
-      store8b(T.v, i, have, make_uint2(vw[0], vw[1]));
-      if (lane == 0) {
-        T.ms[block] = ms;
-        T.vs[block] = vs;
-      }
-    } else {
-      store8<float>(T.m, i, have, m);
-      store8<float>(T.v, i, have, v);
+    for (int j = 0; j < 2; ++j) {
+      const int64_t i = last * kBlock + 128 * j + 4 * lane;
+      const int have = static_cast<int>(min(max(n - i, int64_t(0)), int64_t(4)));
+      store4<typename B::P>(T.p, i, have, now.p[j]);
+      if constexpr (PARAM == kParamMaster) store4<__nv_bfloat16>(T.copy, i, have, now.copy[j]);
+      store4<typename B::S>(T.m, i, have, now.m[j]);
+      store4<typename B::S>(T.v, i, have, now.v[j]);
+    }
+    if (EIGHT && lane == 0) {
+      T.ms[last] = now.ms;
+      T.vs[last] = now.vs;
     }
   }
 }
 
-// The values that 8-bit states stand for.
+// The values that 8-bit states stand for: four per thread and array, four times.
 __global__ void __launch_bounds__(256) k_adamw_values(int64_t n, const uint8_t* m8, const float* ms, const uint8_t* v8,
                                                       const float* vs, float* m_out, float* v_out) {
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
-  if (i >= n) return;
-  const int have = static_cast<int>(min(n - i, int64_t(8)));
-  float m[8], v[8];
-  decode(load8b(m8, i, n, have), load8b(v8, i, n, have), ms[i / kBlock], vs[i / kBlock], m, v);
-  store8<float>(m_out, i, have, m);
-  store8<float>(v_out, i, have, v);
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * 4096 + threadIdx.x * 4;
+  uint32_t mc[4], vc[4];
+  float sm[4], sv[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t i = base + k * 1024;
+    if (i >= n) continue;
+    const int have = static_cast<int>(min(n - i, int64_t(4)));
+    mc[k] = load4<uint8_t>(m8, i, n, have);
+    vc[k] = load4<uint8_t>(v8, i, n, have);
+    sm[k] = ms[i / kBlock];
+    sv[k] = vs[i / kBlock];
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t i = base + k * 1024;
+    if (i >= n) continue;
+    const int have = static_cast<int>(min(n - i, int64_t(4)));
+    f2 m[2], v[2];
+    decode(mc[k], vc[k], f2_dup(unit_m(sm[k])), f2_dup(unit_v(sv[k])), m, v);
+    store4<float>(m_out, i, have, raw_f32(m));
+    store4<float>(v_out, i, have, raw_f32(v));
+  }
 }
 
 template <int PARAM, typename G, bool EIGHT, int CAP>
@@ -301,9 +546,9 @@ cudaError_t launch(const AdamArgs& a, const Scalars& s, int64_t from, int64_t to
   Batch<CAP> b;
   int64_t blocks = 0;
   for (int64_t i = from; i < to; ++i) blocks += ceil_div(a.tensors[i].n, kBlock);
-  // chunks of 8 blocks (one per warp), up to four times that where every SM
-  // still gets several CTAs
-  b.iters = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, blocks / (8 * 16 * num_sms()))));
+  // chunks of one block per warp, up to 16 times that where every SM still gets
+  // several CTAs
+  b.iters = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, blocks / (kWarps * 40 * num_sms()))));
   int64_t chunks = 0;
   b.count = 0;
   for (int64_t i = from; i < to; ++i) {
@@ -311,7 +556,7 @@ cudaError_t launch(const AdamArgs& a, const Scalars& s, int64_t from, int64_t to
     if (t.n == 0) continue;
     b.t[b.count] = t;
     b.first[b.count++] = static_cast<int32_t>(chunks);
-    chunks += ceil_div(ceil_div(t.n, kBlock), 8 * b.iters);
+    chunks += ceil_div(ceil_div(t.n, kBlock), kWarps * b.iters);
   }
   if (b.count == 0) return cudaSuccess;
   if (chunks > INT32_MAX) return cudaErrorInvalidConfiguration;
@@ -321,8 +566,12 @@ cudaError_t launch(const AdamArgs& a, const Scalars& s, int64_t from, int64_t to
   // never a NULL pointer behind a flag: any readable address
   b.clock = a.clock ? reinterpret_cast<const float*>(a.clock + 2) : reinterpret_cast<const float*>(b.t[0].p);
   b.scale = a.scale ? a.scale : reinterpret_cast<const float*>(b.t[0].p);
+  auto kernel = k_adamw<PARAM, G, EIGHT, CAP>;
+  constexpr uint32_t smem = kAheadBlocks<EIGHT> * Place<PARAM, G, EIGHT>::kStage;
+  const cudaError_t e = set_smem(kernel, smem);
+  if (e != cudaSuccess) return e;
   ProfScope prof(QLORA_KC_AUX, st);
-  return launch_pdl(k_adamw<PARAM, G, EIGHT, CAP>, dim3(static_cast<unsigned>(chunks)), dim3(256), 0, st, nullptr, b);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(chunks)), dim3(32 * kWarps), smem, st, nullptr, b);
 }
 
 template <int PARAM, typename G, bool EIGHT>
@@ -373,7 +622,7 @@ cudaError_t launch_adamw(const AdamArgs& a, cudaStream_t st) {
 cudaError_t launch_adamw_values(int64_t n, const uint8_t* m8, const float* ms, const uint8_t* v8, const float* vs,
                                 float* m_out, float* v_out, cudaStream_t st) {
   ProfScope prof(QLORA_KC_AUX, st);
-  return launch_pdl(k_adamw_values, dim3(static_cast<unsigned>(ceil_div(n, 2048))), dim3(256), 0, st, nullptr, n, m8, ms,
+  return launch_pdl(k_adamw_values, dim3(static_cast<unsigned>(ceil_div(n, 4096))), dim3(256), 0, st, nullptr, n, m8, ms,
                     v8, vs, m_out, v_out);
 }
 

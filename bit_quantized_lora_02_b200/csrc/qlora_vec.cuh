@@ -151,6 +151,10 @@ __device__ __forceinline__ void store_raw(T* p, int col, int cols, const uint4& 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+template <int BYTES>   // 4, 8 or 16
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Wait until at most `left` of this thread's latest groups are in flight (0..3).
 __device__ __forceinline__ void cp_async_wait(int left) {
@@ -169,6 +173,22 @@ __device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+template <typename V>
+__device__ __forceinline__ V lds(uint32_t a);
+template <>
+__device__ __forceinline__ uint4 lds<uint4>(uint32_t a) { return lds128(a); }
+template <>
+__device__ __forceinline__ uint2 lds<uint2>(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+template <>
+__device__ __forceinline__ uint32_t lds<uint32_t>(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
 
