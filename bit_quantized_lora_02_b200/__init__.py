@@ -34,7 +34,8 @@ EXPORTS = ("qlora_nf4_sizes", "nf4_quantize", "nf4_quantize_noalloc", "nf4_dequa
            "qlora_linear_bwd_dropout", "qlora_selftest_wait_timeout", "qlora_grouped_workspace_size",
            "qlora_linear_fwd_grouped", "qlora_linear_bwd_grouped",
            "qlora_layer_norm_fwd", "qlora_layer_norm_bwd", "qlora_layer_norm_workspace_size",
-           "qlora_adamw_step", "qlora_adamw_state_values")
+           "qlora_adamw_step", "qlora_adamw_state_values",
+           "qlora_token_logprobs_fwd", "qlora_token_logprobs_bwd")
 
 KERNEL_CLASSES = ("quant", "dq_const", "dequant", "fwd_gemm", "bwd_gemm", "lora_gemm", "aux")
 
@@ -70,6 +71,12 @@ class QloraNorm(ctypes.Structure):
     """Mirror of ``qlora_norm_t``."""
     _fields_ = [("M", ctypes.c_int64), ("D", ctypes.c_int64), ("dtype", ctypes.c_int32), ("wdtype", ctypes.c_int32),
                 ("rms", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class QloraLogits(ctypes.Structure):
+    """Mirror of ``qlora_logits_t``."""
+    _fields_ = [("N", ctypes.c_int64), ("V", ctypes.c_int64), ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("top", ctypes.c_int32)]
 
 
 class QloraAdamWTensor(ctypes.Structure):
@@ -129,6 +136,9 @@ def lib() -> ctypes.CDLL:
     L.qlora_layer_norm_fwd.argtypes = [NP, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.qlora_layer_norm_bwd.argtypes = [NP, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, c_sz, vp]
     L.qlora_layer_norm_workspace_size.argtypes = [NP, c_i32, ctypes.POINTER(c_sz)]
+    LP = ctypes.POINTER(QloraLogits)
+    L.qlora_token_logprobs_fwd.argtypes = [LP, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.qlora_token_logprobs_bwd.argtypes = [LP, vp, vp, vp, vp, vp, vp, vp, c_i64, c_i64, vp]
     L.qlora_adamw_step.argtypes = [ctypes.POINTER(QloraAdamW), ctypes.POINTER(QloraAdamWTensor), c_i64, vp]
     L.qlora_adamw_state_values.argtypes = [c_i64, vp, vp, vp, vp, vp, vp, vp]
     L.qlora_last_error.restype = ctypes.c_char_p
@@ -141,7 +151,8 @@ def lib() -> ctypes.CDLL:
                  "qlora_linear_dropout_workspace_size", "qlora_linear_fwd_dropout", "qlora_linear_bwd_dropout",
                  "qlora_selftest_wait_timeout", "qlora_grouped_workspace_size", "qlora_linear_fwd_grouped",
                  "qlora_linear_bwd_grouped", "qlora_layer_norm_fwd", "qlora_layer_norm_bwd",
-                 "qlora_layer_norm_workspace_size", "qlora_adamw_step", "qlora_adamw_state_values"):
+                 "qlora_layer_norm_workspace_size", "qlora_adamw_step", "qlora_adamw_state_values",
+                 "qlora_token_logprobs_fwd", "qlora_token_logprobs_bwd"):
         getattr(L, name).restype = c_i32
     _lib = L
     return L
@@ -746,6 +757,96 @@ def qlora_layer_norm_bwd(dY: torch.Tensor, S: torch.Tensor, weight: torch.Tensor
     _check(lib().qlora_layer_norm_bwd(ctypes.byref(n), pdY, pS, pw, pm, pr, pdS, pdX, pdw, pdb, workspace.data_ptr(),
                                       _nbytes(workspace), raw))
     return dX, dweight, dbias
+
+
+@dataclass
+class TokenLogprobs:
+    """Results of qlora_token_logprobs_fwd: fp32 (N,) tensors, and (N, top)
+    int32 indices and fp32 log probabilities of the largest logits."""
+    logp: Optional[torch.Tensor]
+    lse: torch.Tensor
+    entropy: Optional[torch.Tensor] = None
+    top_ids: Optional[torch.Tensor] = None
+    top_logp: Optional[torch.Tensor] = None
+
+
+def _logits_struct(logits: torch.Tensor, vocab: Optional[int], top: int) -> QloraLogits:
+    """Rows may lie further apart than they are long; the values of a row are
+    neighbours."""
+    if logits.dim() != 2:
+        raise ValueError(f"logits: shape {tuple(logits.shape)}, expected (tokens, vocabulary)")
+    N, cols = logits.shape
+    V = cols if vocab is None else int(vocab)
+    if not 0 < V <= cols:
+        raise ValueError(f"vocab={V} with {cols} columns of logits")
+    sr, sc = logits.stride()
+    if cols > 1 and sc != 1 or N > 1 and sr < cols:
+        raise ValueError(f"logits: strides {(sr, sc)}, expected rows of neighbouring values that do not overlap")
+    return QloraLogits(N, V, sr if N > 1 else cols, _dt(logits, "logits"), int(top))
+
+
+def qlora_token_logprobs_fwd(logits: torch.Tensor, targets: Optional[torch.Tensor] = None, vocab: Optional[int] = None,
+                             top: int = 0, entropy: bool = False, out: Optional[TokenLogprobs] = None,
+                             stream=None) -> TokenLogprobs:
+    """Log probabilities of the given tokens (int64; a target outside
+    [0, vocab) does not count and gives 0) from bf16 or fp32 logits of shape
+    (tokens, columns), the first `vocab` columns of which count; with the
+    entropy of every row and its `top` (up to 32) most probable tokens, equal
+    logits by ascending index.  `out`: tensors of an earlier call to write to."""
+    l = _logits_struct(logits, vocab, top)
+    N, dev, f32 = logits.shape[0], logits.device, torch.float32
+    pt = _want(targets, "targets", (N,), torch.int64, dev)
+    if out is not None:
+        have = (out.logp is not None, out.entropy is not None, out.top_ids is not None, out.top_logp is not None)
+        if have != (targets is not None, bool(entropy), top > 0, top > 0) or out.lse is None:
+            raise ValueError("out holds other results than the call asks for")
+        _want(out.logp, "out.logp", (N,), f32, dev), _want(out.lse, "out.lse", (N,), f32, dev)
+        _want(out.entropy, "out.entropy", (N,), f32, dev)
+        _want(out.top_ids, "out.top_ids", (N, top), torch.int32, dev)
+        _want(out.top_logp, "out.top_logp", (N, top), f32, dev)
+    _on_cuda(logits, "logits")
+    raw, own = _enter(dev, stream)
+    if out is None:
+        with own:
+            out = TokenLogprobs(torch.empty(N, dtype=f32, device=dev) if targets is not None else None,
+                                torch.empty(N, dtype=f32, device=dev),
+                                torch.empty(N, dtype=f32, device=dev) if entropy else None,
+                                torch.empty(N, top, dtype=torch.int32, device=dev) if top > 0 else None,
+                                torch.empty(N, top, dtype=f32, device=dev) if top > 0 else None)
+    _check(lib().qlora_token_logprobs_fwd(ctypes.byref(l), logits.data_ptr(), pt, _ptr(out.logp), out.lse.data_ptr(),
+                                          _ptr(out.entropy), _ptr(out.top_ids), _ptr(out.top_logp), raw))
+    return out
+
+
+def qlora_token_logprobs_bwd(logits: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor, dlogp: torch.Tensor,
+                             entropy: Optional[torch.Tensor] = None, dentropy: Optional[torch.Tensor] = None,
+                             vocab: Optional[int] = None, dlogits: Optional[torch.Tensor] = None,
+                             stream=None) -> torch.Tensor:
+    """Gradient of the logits from the gradients of qlora_token_logprobs_fwd's
+    logp and (with its entropy) entropy.  Columns from `vocab` on get zeros.
+    `dlogits` may be the logits themselves (in place)."""
+    l = _logits_struct(logits, vocab, 0)
+    (N, cols), dev, f32 = logits.shape, logits.device, torch.float32
+    for t, name in ((targets, "targets"), (lse, "lse"), (dlogp, "dlogp")):
+        if t is None:
+            raise ValueError(f"{name} is required")
+    if dentropy is not None and entropy is None:
+        raise ValueError("dentropy needs entropy")
+    pt, pl = _want(targets, "targets", (N,), torch.int64, dev), _want(lse, "lse", (N,), f32, dev)
+    pd = _want(dlogp, "dlogp", (N,), f32, dev)
+    pe, ph = _want(entropy, "entropy", (N,), f32, dev), _want(dentropy, "dentropy", (N,), f32, dev)
+    if dlogits is not None:
+        if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape or dlogits.device != dev:
+            raise ValueError("dlogits must have the logits' shape, dtype and device")
+        _logits_struct(dlogits, vocab, 0)
+    _on_cuda(logits, "logits")
+    raw, own = _enter(dev, stream)
+    if dlogits is None:
+        with own:
+            dlogits = torch.empty(N, cols, dtype=logits.dtype, device=dev)
+    _check(lib().qlora_token_logprobs_bwd(ctypes.byref(l), logits.data_ptr(), pt, pl, pd, pe, ph, dlogits.data_ptr(),
+                                          cols, dlogits.stride(0) if N > 1 else cols, raw))
+    return dlogits
 
 
 ADAMW_BLOCK = 256       # values that share one scale of an 8-bit state

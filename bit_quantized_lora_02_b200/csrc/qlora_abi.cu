@@ -638,6 +638,79 @@ int qlora_layer_norm_bwd(const qlora_norm_t* n, const void* dY, const void* S, c
   return check_cuda(launch_norm_bwd(a, static_cast<cudaStream_t>(stream)), "qlora_layer_norm_bwd launch");
 }
 
+static int check_logits(const qlora_logits_t* l) {
+  if (!l) return fail(QLORA_ERR_INVALID_ARG, "logits descriptor is NULL");
+  if (l->N < 0 || l->V < 1 || l->ld < l->V)
+    return fail(QLORA_ERR_INVALID_ARG, "bad shape N=%lld V=%lld ld=%lld", (long long)l->N, (long long)l->V, (long long)l->ld);
+  if (l->V > (int64_t(1) << 30) || l->N > (int64_t(1) << 31)) return fail(QLORA_ERR_UNSUPPORTED, "V above 2^30 or N above 2^31");
+  int64_t n = 0;
+  if (!elem_count(l->N, l->ld, &n)) return fail(QLORA_ERR_INVALID_ARG, "N * ld overflows");
+  if (l->dtype < 0 || l->dtype > 1) return fail(QLORA_ERR_INVALID_ARG, "dtype must be QLORA_DT_BF16 or QLORA_DT_F32");
+  if (l->top < 0 || l->top > kLogpMaxTop) return fail(QLORA_ERR_UNSUPPORTED, "top=%d outside 0..%d", l->top, kLogpMaxTop);
+  if (l->top > l->V) return fail(QLORA_ERR_INVALID_ARG, "top=%d above V=%lld", l->top, (long long)l->V);
+  return QLORA_OK;
+}
+
+static int check_ptr(const void* p, size_t al, const char* name, bool required) {
+  if (!p) return required ? fail(QLORA_ERR_INVALID_ARG, "%s is NULL", name) : QLORA_OK;
+  if (!aligned(p, al)) return fail(QLORA_ERR_ALIGNMENT, "%s must be %zu-byte aligned", name, al);
+  return QLORA_OK;
+}
+
+static LogpArgs logp_args(const qlora_logits_t* l, const void* logits, const int64_t* targets) {
+  LogpArgs a{};
+  a.N = l->N; a.ld = l->ld; a.V = static_cast<int>(l->V); a.dtype = l->dtype; a.top = l->top;
+  a.logits = logits; a.targets = targets; a.split = 1;
+  return a;
+}
+
+int qlora_token_logprobs_fwd(const qlora_logits_t* l, const void* logits, const int64_t* targets, float* logp,
+                             float* lse, float* entropy, int32_t* top_ids, float* top_logp, qlora_stream_t stream) {
+  int rc = check_logits(l);
+  if (rc) return rc;
+  if ((targets == nullptr) != (logp == nullptr) && l->N > 0)
+    return fail(QLORA_ERR_INVALID_ARG, "logp goes with targets: both or neither");
+  if ((l->top > 0) != (top_ids != nullptr) || (l->top > 0) != (top_logp != nullptr)) {
+    if (l->N > 0) return fail(QLORA_ERR_INVALID_ARG, "top_ids and top_logp go with top > 0");
+  }
+  if (l->N == 0) return ok();
+  if ((rc = check_ptr(logits, l->dtype == QLORA_DT_BF16 ? 2 : 4, "logits", true)) ||
+      (rc = check_ptr(targets, 8, "targets", false)) || (rc = check_ptr(logp, 4, "logp", false)) ||
+      (rc = check_ptr(lse, 4, "lse", true)) || (rc = check_ptr(entropy, 4, "entropy", false)) ||
+      (rc = check_ptr(top_ids, 4, "top_ids", false)) || (rc = check_ptr(top_logp, 4, "top_logp", false)))
+    return rc;
+  DeviceScope scope;
+  if ((rc = scope.bind(logits))) return rc;
+  LogpArgs a = logp_args(l, logits, targets);
+  a.logp = logp; a.lse = lse; a.entropy = entropy; a.top_ids = top_ids; a.top_logp = top_logp;
+  return check_cuda(launch_logp_fwd(a, static_cast<cudaStream_t>(stream)), "qlora_token_logprobs_fwd launch");
+}
+
+int qlora_token_logprobs_bwd(const qlora_logits_t* l, const void* logits, const int64_t* targets, const float* lse,
+                             const float* dlogp, const float* entropy, const float* dentropy, void* dlogits,
+                             int64_t cols, int64_t ldd, qlora_stream_t stream) {
+  int rc = check_logits(l);
+  if (rc) return rc;
+  int64_t n = 0;
+  if (cols < l->V || cols > (int64_t(1) << 30) || ldd < cols || !elem_count(l->N, ldd, &n))
+    return fail(QLORA_ERR_INVALID_ARG, "bad gradient shape cols=%lld ldd=%lld", (long long)cols, (long long)ldd);
+  if (l->N == 0) return ok();
+  if (dentropy && !entropy) return fail(QLORA_ERR_INVALID_ARG, "dentropy needs entropy");
+  const size_t e = l->dtype == QLORA_DT_BF16 ? 2 : 4;
+  if ((rc = check_ptr(logits, e, "logits", true)) || (rc = check_ptr(targets, 8, "targets", true)) ||
+      (rc = check_ptr(lse, 4, "lse", true)) || (rc = check_ptr(dlogp, 4, "dlogp", true)) ||
+      (rc = check_ptr(entropy, 4, "entropy", false)) || (rc = check_ptr(dentropy, 4, "dentropy", false)) ||
+      (rc = check_ptr(dlogits, e, "dlogits", true)))
+    return rc;
+  if (dlogits == logits && ldd != l->ld) return fail(QLORA_ERR_INVALID_ARG, "in place, ldd must be ld");
+  DeviceScope scope;
+  if ((rc = scope.bind(logits))) return rc;
+  LogpArgs a = logp_args(l, logits, targets);
+  a.lse_in = lse; a.dlogp = dlogp; a.entropy_in = entropy; a.dentropy = dentropy;
+  a.dlogits = dlogits; a.cols = static_cast<int>(cols); a.ldd = ldd;
+  return check_cuda(launch_logp_bwd(a, static_cast<cudaStream_t>(stream)), "qlora_token_logprobs_bwd launch");
+}
+
 int qlora_adamw_step(const qlora_adamw_t* o, const qlora_adamw_tensor_t* tensors, int64_t count,
                      qlora_stream_t stream) {
   static_assert(sizeof(qlora_adamw_tensor_t) == sizeof(AdamTensor), "a tensor's descriptor is copied as it is");

@@ -74,6 +74,25 @@ size_t norm_workspace_bytes(int64_t M, int64_t D, int dtype, bool dbias);
 cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t st);
 cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t st);
 
+// log probabilities of given tokens (qlora_logprob.cu)
+constexpr int kLogpMaxTop = 32;
+struct LogpArgs {
+  int64_t N, ld;
+  int V, dtype, top;
+  const void* logits;
+  const int64_t* targets;   // forward: or nullptr, with logp
+  float *logp, *lse, *entropy, *top_logp;
+  int32_t* top_ids;
+  int split;                // forward: CTAs of a cluster per row
+  // backward (entropy_in and dentropy: both or nullptr)
+  const float *lse_in, *dlogp, *entropy_in, *dentropy;
+  void* dlogits;
+  int64_t ldd;
+  int cols;
+};
+cudaError_t launch_logp_fwd(const LogpArgs& a, cudaStream_t st);
+cudaError_t launch_logp_bwd(const LogpArgs& a, cudaStream_t st);
+
 // AdamW over many tensors (qlora_adamw.cu)
 struct AdamTensor {
   void* p;             // parameter (bf16, or fp32)

@@ -368,6 +368,48 @@ int qlora_layer_norm_bwd(const qlora_norm_t *n, const void *dY, const void *S, c
                          const float *rstd, const void *dS, void *dX, float *dweight, float *dbias, void *workspace,
                          size_t workspace_bytes, qlora_stream_t stream);
 
+/* Log probabilities of given tokens from a model's logits (the loss of a
+ * fine-tuning step and of preference methods is a sum of them), with the
+ * entropy of each row's distribution and its most probable tokens. */
+#define QLORA_LOGPROBS_MAX_TOP 32
+typedef struct {
+  int64_t N;       /* rows (tokens), >= 0                                        */
+  int64_t V;       /* logits of a row that count (the vocabulary), 1 .. 2^30     */
+  int64_t ld;      /* values from one row's start to the next one's, >= V; the   *
+                    * columns past V (a padded vocabulary) are not read          */
+  int32_t dtype;   /* QLORA_DT_* of the logits and of their gradient, aligned to *
+                    * their own size                                             */
+  int32_t top;     /* alternatives per row, 0 .. 32 and at most V                */
+} qlora_logits_t;
+
+/* Forward, per row of logits z:
+ *     lse = log sum exp(z),   logp = z[target] - lse,
+ *     entropy = -sum p log p  with p = exp(z - lse).
+ *   targets  : N int64, or NULL together with logp.  A target outside [0, V)
+ *              (a prompt position, say) does not count: its logp is 0.
+ *   logp     : N fp32.   lse : N fp32, for the backward pass.
+ *   entropy  : N fp32 or NULL.
+ *   top_ids, top_logp : N x top (int32, fp32), the `top` largest logits in
+ *              descending order, equal ones by ascending index, and their log
+ *              probabilities; NULL when top is 0.
+ * Logits of -infinity (masked tokens) have probability 0.  A row of nothing else
+ * has lse = logp = top_logp = -infinity and entropy 0.  A NaN or +infinity makes
+ * the row's values NaN (lse too); its top_ids are then unspecified indices. */
+int qlora_token_logprobs_fwd(const qlora_logits_t *l, const void *logits, const int64_t *targets, float *logp,
+                             float *lse, float *entropy, int32_t *top_ids, float *top_logp, qlora_stream_t stream);
+
+/* Backward: with p = exp(z - lse),
+ *     dz[j] = dlogp (1[j = target] - p[j]) - dentropy p[j] (log p[j] + entropy).
+ *   lse, entropy : as the forward wrote them.   dlogp : N fp32.
+ *   dentropy : N fp32 or NULL; needs entropy (else entropy may be NULL).
+ *   dlogits  : N rows of `cols` >= V values, `ldd` >= cols apart, written whole
+ *              (zeros from column V on).  May be the logits' memory when ldd = ld.
+ * Rows whose target does not count have dlogp taken as 0; rows of -infinity
+ * only get zeros. */
+int qlora_token_logprobs_bwd(const qlora_logits_t *l, const void *logits, const int64_t *targets, const float *lse,
+                             const float *dlogp, const float *entropy, const float *dentropy, void *dlogits,
+                             int64_t cols, int64_t ldd, qlora_stream_t stream);
+
 /* One AdamW step over many tensors at once (Loshchilov and Hutter, "Decoupled
  * Weight Decay Regularization", ICLR 2019), for the adapters that
  * qlora_linear_bwd gives the gradients of:

@@ -176,3 +176,67 @@ def test_adamw_oracle_step():
     0.05, v' = 0.00025, both corrected to 0.5 and 0.25, so the update is lr."""
     p, m, v = SO.adamw_param(np.array([1.0]), np.zeros(1), np.zeros(1), np.array([0.5]), 1, 0.1, 0.9, 0.999, 0.0, 0.2)
     assert np.allclose(p, 1.0 * (1 - 0.02) - 0.1) and np.allclose(m, 0.05) and np.allclose(v, 0.00025)
+
+
+# ---------------------------------------------------------------------------
+# log probabilities of given tokens
+# ---------------------------------------------------------------------------
+def test_logprobs_refusals_of_the_binding():
+    z, t = torch.zeros(4, 64, dtype=BF16), torch.zeros(4, dtype=torch.int64)
+    s = torch.zeros(4)
+    for args, kw, match in (((z, t), {}, "must be on a CUDA device"), ((z, t.int()), {}, "targets: dtype"),
+                            ((z, t[:3]), {}, "targets: shape"), ((z[0], t), {}, "expected \\(tokens, vocabulary\\)"),
+                            ((z, t), dict(vocab=65), "vocab=65"), ((z, t), dict(vocab=0), "vocab=0"),
+                            ((torch.zeros(64, 4, dtype=BF16).t(), t), {}, "strides"),
+                            ((torch.zeros(1, 64).expand(4, 64), t), {}, "strides"),
+                            ((z.half(), t), {}, "logits: dtype"),
+                            ((z, t), dict(out=Q.TokenLogprobs(s, s), entropy=True), "other results"),
+                            ((z, t), dict(out=Q.TokenLogprobs(s[:3], s)), "out.logp: shape")):
+        with pytest.raises(ValueError, match=match):
+            Q.qlora_token_logprobs_fwd(*args, **kw)
+    for args, kw, match in (((z, t, s, s), {}, "must be on a CUDA device"), ((z, t, s, None), {}, "dlogp is required"),
+                            ((z, t, s, s), dict(dentropy=s), "dentropy needs entropy"),
+                            ((z, t, s[:2], s), {}, "lse: shape"), ((z, t, s, s.double()), {}, "dlogp: dtype"),
+                            ((z, t, s, s), dict(dlogits=torch.zeros(4, 64)), "dlogits must have")):
+        with pytest.raises(ValueError, match=match):
+            Q.qlora_token_logprobs_bwd(*args, **kw)
+
+
+def test_logprobs_refusals_of_the_library(L):
+    def d(N=4, V=100, ld=100, dt=0, top=0):
+        return ctypes.byref(Q.QloraLogits(N, V, ld, dt, top))
+
+    def fwd(l, z=0x1000, t=0x2000, logp=0x3000, lse=0x4000, ent=None, ids=None, tl=None):
+        return L.qlora_token_logprobs_fwd(l, z, t, logp, lse, ent, ids, tl, None)
+    assert fwd(None) == -1 and fwd(d(N=-1)) == -1 and fwd(d(V=0)) == -1 and fwd(d(ld=99)) == -1 and fwd(d(dt=2)) == -1
+    assert fwd(d(V=(1 << 30) + 1, ld=1 << 31)) == -2 and fwd(d(N=1 << 31, ld=1 << 40)) == -1
+    assert fwd(d(top=33), ids=0x5000, tl=0x6000) == -2 and fwd(d(V=3, ld=3, top=4), ids=0x5000, tl=0x6000) == -1
+    assert fwd(d(top=1)) == -1 and fwd(d(), ids=0x5000) == -1 and fwd(d(top=1), ids=0x5000) == -1
+    assert fwd(d(), z=None) == -1 and fwd(d(), t=None) == -1 and fwd(d(), logp=None) == -1 and fwd(d(), lse=None) == -1
+    assert fwd(d(), z=0x1001) == -3 and fwd(d(dt=1), z=0x1002) == -3 and fwd(d(), t=0x2004) == -3 and fwd(d(), ent=0x7002) == -3
+    assert fwd(d(N=0), z=None, t=None, logp=None, lse=None) == 0
+
+    def bwd(l, z=0x1000, t=0x2000, lse=0x3000, dl=0x4000, ent=None, dh=None, out=0x5000, cols=100, ldd=100):
+        return L.qlora_token_logprobs_bwd(l, z, t, lse, dl, ent, dh, out, cols, ldd, None)
+    assert bwd(d(), cols=99) == -1 and bwd(d(), ldd=99) == -1 and bwd(d(), dh=0x6000) == -1
+    assert bwd(d(), t=None) == -1 and bwd(d(), dl=None) == -1 and bwd(d(), out=None) == -1 and bwd(d(), out=0x5001) == -3
+    assert bwd(d(), out=0x1000, ldd=104) == -1                            # in place with other strides
+    assert bwd(d(N=0), z=None, t=None, lse=None, dl=None, out=None) == 0
+
+
+def test_logprobs_oracle():
+    """The plain forward against torch's log_softmax in 64 bits, and the plain
+    backward against its autograd."""
+    z = torch.randn(5, 37, dtype=torch.float64, requires_grad=True)
+    t = torch.tensor([3, 36, -100, 0, 37])
+    ref = SO.token_logprobs(z.detach().numpy(), t.numpy(), top=4)
+    q = torch.log_softmax(z, 1)
+    counts = (t >= 0) & (t < 37)
+    logp = torch.where(counts, q.gather(1, t.clamp(0, 36)[:, None])[:, 0], 0.0)
+    ent = -(q.exp() * q).sum(1)
+    assert np.allclose(ref["logp"], logp.detach().numpy(), atol=1e-12) and np.allclose(ref["entropy"], ent.detach().numpy(), atol=1e-12)
+    assert np.array_equal(ref["top_ids"], torch.topk(z, 4, 1).indices.numpy())
+    a, b = torch.randn(5, dtype=torch.float64), torch.randn(5, dtype=torch.float64)
+    ((logp * a).sum() + (ent * b).sum()).backward()
+    got = SO.token_logprobs_backward(z.detach().numpy(), t.numpy(), ref["lse"], a.numpy(), ref["entropy"], b.numpy())
+    assert np.allclose(got, z.grad.numpy(), atol=1e-12)
