@@ -83,7 +83,7 @@ struct LogpArgs {
   const int64_t* targets;   // forward: or nullptr, with logp
   float *logp, *lse, *entropy, *top_logp;
   int32_t* top_ids;
-  int split;                // forward: CTAs of a cluster per row
+  int split, split_log2;    // forward: CTAs of a cluster per row (a power of two)
   // backward (entropy_in and dentropy: both or nullptr)
   const float *lse_in, *dlogp, *entropy_in, *dentropy;
   void* dlogits;

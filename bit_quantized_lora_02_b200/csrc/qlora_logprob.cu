@@ -10,16 +10,19 @@
 //
 // Forward, one pass over the row: each thread keeps a running maximum with S and
 // G relative to it and rescales them when a batch of 4 x 16 bytes raises the
-// maximum; the threads' triples are then merged.  Few rows are split over
-// clusters of up to 8 CTAs, whose results meet in the first one's shared memory.
+// maximum; the threads' triples are then merged.  (Folding the difference and the
+// factor log2 e into one fused multiply-add saved no time and cost the exact 0 of
+// a certain token's logp.)  Few rows are split over clusters of up to 8 CTAs,
+// whose results meet in the first one's shared memory.
 //
 // Top alternatives without a second pass over memory: the threads' maxima give
-// those of 32 groups of threads, and the top-th largest of these is a bound T
-// that at least `top` logits reach.  Only threads whose own maximum reaches T
-// look through their logits again (L2) and list what reaches it: about
-// 32 log(32 / (32 - top)) logits of distinct values.  A rank count over the list orders it,
-// equal logits by their index.  Lists that overflow (rows with few distinct
-// values, as under a mask) take `collect_many`.
+// those of 32 groups of threads, and the top-th largest of these is a bound that
+// at least `top` logits reach (of distinct values about 32 log(32 / (32 - top))).
+// Only threads whose own maximum reaches it have such logits: their windows are
+// shared out over the CTA and loaded again (from L2), those that reach the bound
+// are shared out by element, and a rank count orders the list, equal logits by
+// their index.  Lists that overflow (rows with few distinct values, as under a
+// mask) take `collect_many`.
 //
 // Bound: HBM in the backward pass (read and write once) and, in bf16, the issue
 // rate in the forward pass: 2 bytes per logit leave 11 instructions for each.
@@ -107,7 +110,7 @@ __device__ __forceinline__ float batch_max(const uint4 (&v)[B]) {
   }
 }
 
-// m, S and G of some logits; m starts at the lowest finite value, so that
+// m, S and G of some logits.  m starts at the lowest finite value, so that
 // differences from it stay defined for logits of -infinity.
 struct Sums {
   float m, s, g;
@@ -128,8 +131,7 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 __device__ __forceinline__ Sums warp_merge(Sums a, bool ent) {
-  const float M = warp_max(a.m);
-  a.rebase(M, ent);
+  a.rebase(warp_max(a.m), ent);
   a.s = warp_sum(a.s);
   if (ent) a.g = warp_sum(a.g);
   return a;
@@ -147,51 +149,72 @@ __device__ __forceinline__ float value_of(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-struct Entry {
-  uint32_t key;
-  int32_t idx;
-};
-__device__ __forceinline__ bool before(const Entry& a, const Entry& b) {
-  return a.key > b.key || (a.key == b.key && a.idx < b.idx);
+// A logit in the list of candidates: its key above the complement of its index,
+// so that a larger entry comes first.
+using Entry = uint64_t;
+__device__ __forceinline__ Entry entry(uint32_t key, int idx) {
+  return (static_cast<uint64_t>(key) << 32) | static_cast<uint32_t>(~idx);
 }
+__device__ __forceinline__ uint32_t entry_key(Entry e) { return static_cast<uint32_t>(e >> 32); }
+__device__ __forceinline__ int entry_idx(Entry e) { return static_cast<int>(~static_cast<uint32_t>(e)); }
 
-struct Shared {
-  Sums part[32];
+struct SharedTop {
   uint32_t group[kGroups];
   Entry list[kCap];
   Entry best[kGroups];
+  Entry bests[8 * kGroups];   // what the cluster's CTAs send to its first
   int count;
-  uint32_t bound;
-  // what the cluster's CTAs send to its first
-  Sums all[8];
-  Entry bests[8 * kGroups];
+  int threads, windows;       // entries of the two lists below
+  uint16_t thread[1024];      // whose maximum reaches the bound
+  int window[kCap];           // of theirs, that reach it
+};
+struct SharedSums {
+  Sums part[2][32];
+  Sums all[8];                // what the cluster's CTAs send to its first
 };
 
-// Every logit of this thread's windows whose key is >= T (or > T) into the list.
-template <typename T, int NT>
-__device__ __forceinline__ void list_own(const Row<T>& row, int w0, int w1, uint32_t T_, bool strict, Shared& sm) {
-  for (int w = w0 + threadIdx.x; w < w1; w += NT) {
-    float x[Row<T>::N];
-    Vec<T>::unpack(row.load(w), x);
+// The logits of one window whose keys are >= least into the list.
+template <typename T>
+__device__ __noinline__ void list_window(uint4 v, int col, int V, uint32_t least, SharedTop* sm) {
+  float z[Row<T>::N];
+  Vec<T>::unpack(v, z);
 #pragma unroll
-    for (int i = 0; i < Row<T>::N; ++i) {
-      const uint32_t k = key_of(x[i]);
-      const int c = row.col(w) + i;
-      if ((strict ? k > T_ : k >= T_) && c >= 0 && c < row.V) {
-        const int at = atomicAdd(&sm.count, 1);
-        if (at < kCap) sm.list[at] = {k, c};
-      }
+  for (int i = 0; i < Row<T>::N; ++i) {
+    const uint32_t k = key_of(z[i]);
+    if (k >= least && col + i >= 0 && col + i < V) {
+      const int at = atomicAdd(&sm->count, 1);
+      if (at < kCap) sm->list[at] = entry(k, col + i);
     }
   }
 }
 
-// The list's `n` entries in order into `best` (the first `top` of them).
+// Every logit of this thread's windows whose key is >= bound (strict: > bound,
+// which is never the largest key).  Eight windows are loaded at a time; most are
+// dismissed by their largest logit.
+template <typename T, int NT>
+__device__ __forceinline__ void list_own(const Row<T>& row, int w0, int w1, uint32_t bound, bool strict, SharedTop& sm) {
+  const uint32_t least = strict ? bound + 1 : bound;
+  for (int w = w0 + threadIdx.x; w < w1; w += 8 * NT) {
+    uint4 v[8];
+    const uint32_t f = minus_inf_word<T>();
+#pragma unroll
+    for (int b = 0; b < 8; ++b) v[b] = w + b * NT < w1 ? row.load(w + b * NT) : make_uint4(f, f, f, f);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      const uint4 one[1] = {v[b]};
+      if (w + b * NT < w1 && key_of(batch_max<T>(one)) >= least) list_window<T>(v[b], row.col(w + b * NT), row.V, least, &sm);
+    }
+  }
+}
+
+// The first `top` of the list's `n` entries, in order, into `best`.
 template <int NT>
 __device__ __forceinline__ void rank_list(int n, int top, const Entry* list, Entry* best) {
   for (int i = threadIdx.x; i < n; i += NT) {
     const Entry e = list[i];
     int r = 0;
-    for (int j = 0; j < n && r < top; ++j) r += before(list[j], e);
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) r += list[j] > e;
     if (r < top) best[r] = e;
   }
 }
@@ -202,19 +225,19 @@ __device__ __forceinline__ void rank_list(int n, int top, const Entry* list, Ent
 // bound, in order of their index.
 template <typename T, int NT>
 __device__ __noinline__ void collect_many(const Row<T>& row, int w0, int w1, int top, uint32_t bound, float mine,
-                                          Shared& sm) {
+                                          SharedTop& sm) {
   int n;
   while (true) {
     __syncthreads();
     if (threadIdx.x == 0) sm.count = 0;
     __syncthreads();
-    if (key_of(mine) >= bound) list_own<T, NT>(row, w0, w1, bound, true, sm);
+    if (bound != 0xFFFFFFFFu && key_of(mine) >= bound) list_own<T, NT>(row, w0, w1, bound, true, sm);
     __syncthreads();
     n = sm.count;
     if (n <= kCap) break;
     rank_list<NT>(kCap, top, sm.list, sm.best);
     __syncthreads();
-    bound = sm.best[top - 1].key;
+    bound = entry_key(sm.best[top - 1]);
   }
   rank_list<NT>(n, top, sm.list, sm.best);
   if (n >= top) return;
@@ -238,7 +261,7 @@ __device__ __noinline__ void collect_many(const Row<T>& row, int w0, int w1, int
         if (lane >= o) sum += y;
       }
       int at = n + sum - __popc(hits);
-      for (uint32_t h = hits; h && at < top; h &= h - 1, ++at) sm.best[at] = {bound, row.col(w + lane) + __ffs(h) - 1};
+      for (uint32_t h = hits; h && at < top; h &= h - 1, ++at) sm.best[at] = entry(bound, row.col(w + lane) + __ffs(h) - 1);
       n += __shfl_sync(0xffffffffu, sum, 31);
     }
   }
@@ -260,21 +283,81 @@ __device__ __forceinline__ void st_first(void* p, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
 }
 
+constexpr int logp_ctas(int nt) { return nt >= 1024 ? 1 : nt == 32 ? 16 : 1024 / nt; }   // CTAs per SM
+constexpr int kStages = 2;       // batches that a thread's loads run ahead (three leave too little L1: 2 to 13% slower)
+
+// CTAs walk over rows gridDim apart; `split` CTAs of a cluster share a row.  The
+// loads run ahead, from one row into the next, through a ring in shared memory
+// (cp.async) in which each thread reads back only what it copied itself: so the
+// end of a row, its merges and its top list, passes while the next row arrives.
 template <typename T, int NT, bool ENT, bool TOP>
-__global__ void __launch_bounds__(NT) k_logp_fwd(LogpArgs a) {
+__global__ void __launch_bounds__(NT, logp_ctas(NT)) k_logp_fwd(LogpArgs a) {
   constexpr int N = Vec<T>::N;
-  __shared__ Shared sm;
+  constexpr uint32_t kStage = kBatch * NT * 16;
+  extern __shared__ __align__(16) uint8_t smem[];
+  SharedSums& sums = *reinterpret_cast<SharedSums*>(smem + kStages * kStage);
+  SharedTop& tops = *reinterpret_cast<SharedTop*>(smem + kStages * kStage + sizeof(SharedSums));   // only with TOP
   const int parts = a.split;
   const int part = parts > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t first = blockIdx.x >> a.split_log2, stride = gridDim.x >> a.split_log2;
+  const uint32_t slot = smem_u32(smem) + threadIdx.x * 16u;
+  const uint32_t ninf = minus_inf_word<T>();
   griddep_launch_dependents();
   griddep_wait();
   if (parts > 1) cluster_sync();   // every CTA runs before one writes to another
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) / parts; r < a.N; r += gridDim.x / parts) {
-    const Row<T> row(reinterpret_cast<const T*>(a.logits) + r * a.ld, a.V);
-    const int nw = row.windows();
-    const int per = (nw + parts - 1) / parts;
-    const int w0 = part * per, w1 = min(nw, w0 + per);
+
+  auto row_at = [&](int64_t r) { return Row<T>(reinterpret_cast<const T*>(a.logits) + r * a.ld, a.V); };
+  auto windows_of = [&](const Row<T>& row, int& w0, int& w1) {
+    const int nw = row.windows(), per = (nw + parts - 1) >> a.split_log2;
+    w0 = part * per;
+    w1 = min(nw, w0 + per);
+  };
+  auto has_edges = [&](const Row<T>& row) { return row.sh != 0 || (row.V + row.sh) % N != 0; };
+  // what is copied next: batch `bw` (its first window) of row `br`
+  int64_t br = first;
+  Row<T> brow = row_at(br < a.N ? br : 0);
+  int bw, bw1;
+  windows_of(brow, bw, bw1);
+  bool bedges = has_edges(brow);
+  auto issue = [&](uint32_t stage) {
+    if (br < a.N) {
+      const T* src = brow.p + brow.col(bw + threadIdx.x);
+      if (!bedges && bw + kBatch * NT <= bw1) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) cp_async16(slot + stage + b * NT * 16, src + b * NT * N, 16);
+      } else {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int w = bw + b * NT + threadIdx.x;
+          const uint32_t dst = slot + stage + b * NT * 16;
+          if (w < bw1) {
+            // a window that starts in the row before reads that row's end too
+            cp_async16(dst, src + b * NT * N, min(a.V - brow.col(w), N) * static_cast<int>(sizeof(T)));
+          } else {
+            sts128(dst, make_uint4(ninf, ninf, ninf, ninf));
+          }
+        }
+      }
+      bw += kBatch * NT;
+      if (bw >= bw1) {
+        br += stride;
+        brow = row_at(br < a.N ? br : 0);
+        windows_of(brow, bw, bw1);
+        bedges = has_edges(brow);
+      }
+    }
+    cp_async_commit();
+  };
+  for (int k = 0; k < kStages; ++k) issue(k * kStage);
+
+  uint32_t stage = 0;
+  int buf = 0;
+  for (int64_t r = first; r < a.N; r += stride, buf ^= 1) {
+    const Row<T> row = row_at(r);
+    int w0, w1;
+    windows_of(row, w0, w1);
+    const bool edges = has_edges(row);
     // the given token's logit, early
     float zt = 0.0f;
     bool counts = false;
@@ -284,16 +367,32 @@ __global__ void __launch_bounds__(NT) k_logp_fwd(LogpArgs a) {
       counts = t >= 0 && t < a.V;
       if (counts) zt = to_f32(row.p[t]);
     }
-    if (TOP && threadIdx.x == 0) sm.count = 0;
-    if (TOP && threadIdx.x < kGroups) sm.best[threadIdx.x] = {0u, 0};   // rows with NaN may not fill it
+    if (TOP && threadIdx.x == 0) tops.count = tops.threads = tops.windows = 0;
+    if (TOP && threadIdx.x < kGroups) tops.best[threadIdx.x] = entry(0u, 0);   // rows with NaN may not fill it
 
     Sums acc = Sums::none();
     f2 s2 = 0, g2 = 0;
-    for (int w = w0 + threadIdx.x; w < w1; w += NT * kBatch) {
+    for (int w = w0; w < w1; w += NT * kBatch) {
       uint4 v[kBatch];
-      const uint32_t f = minus_inf_word<T>();
+      cp_async_wait(kStages - 1);
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) v[b] = w + b * NT < w1 ? row.load(w + b * NT) : make_uint4(f, f, f, f);
+      for (int b = 0; b < kBatch; ++b) v[b] = lds128(slot + stage + b * NT * 16);
+      if (edges) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int c = row.col(w + b * NT + threadIdx.x);
+          if (c < 0 || (c < row.V && c + N > row.V)) {   // values outside the row
+            float x[N];
+            Vec<T>::unpack(v[b], x);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              if (c + i < 0 || c + i >= row.V) x[i] = __uint_as_float(0xFF800000u);
+            v[b] = Vec<T>::pack(x);
+          }
+        }
+      }
+      issue(stage);
+      stage = stage == (kStages - 1) * kStage ? 0 : stage + kStage;
       const float top = batch_max<T>(v);
       if (top > acc.m) {
         acc.s = f2_sum(s2);
@@ -333,17 +432,24 @@ __global__ void __launch_bounds__(NT) k_logp_fwd(LogpArgs a) {
       uint32_t k = mine > kLowest ? key_of(mine) : 0u;
 #pragma unroll
       for (int o = PER / 2; o; o >>= 1) k = max(k, __shfl_xor_sync(0xffffffffu, k, o));
-      if (threadIdx.x % PER == 0) sm.group[threadIdx.x / PER] = k;
+      if (threadIdx.x % PER == 0) tops.group[threadIdx.x / PER] = k;
     }
-    acc = warp_merge(acc, ENT);
-    if (lane == 0) sm.part[warp] = acc;
-    __syncthreads();
-    Sums all = Sums::none();
-    if (lane < NT / 32) all = sm.part[lane];
-    all = warp_merge(all, ENT);
+    Sums all = warp_merge(acc, ENT);
+    if (NT > 32) {
+      // two scratches in turn: the next row's partial results cannot meet this row's readers
+      if (lane == 0) sums.part[buf][warp] = all;
+      __syncthreads();
+      if (TOP || parts > 1 || warp == 0) {
+        all = Sums::none();
+        if (lane < NT / 32) all = sums.part[buf][lane];
+        all = warp_merge(all, ENT);
+      }
+    } else {
+      __syncwarp();
+    }
 
     if (TOP) {
-      const uint32_t g = sm.group[lane];
+      const uint32_t g = tops.group[lane];
       int rank = 0;
 #pragma unroll
       for (int j = 0; j < kGroups; ++j) {
@@ -352,132 +458,237 @@ __global__ void __launch_bounds__(NT) k_logp_fwd(LogpArgs a) {
       }
       const uint32_t who = __ballot_sync(0xffffffffu, rank == a.top - 1);
       const uint32_t bound = __shfl_sync(0xffffffffu, g, __ffs(who) - 1);
-      if (key_of(mine) >= bound) list_own<T, NT>(row, w0, w1, bound, false, sm);
+      if (key_of(mine) >= bound) tops.thread[atomicAdd(&tops.threads, 1)] = static_cast<uint16_t>(threadIdx.x);
       __syncthreads();
-      const int n = sm.count;
+      // their windows, one per thread
+      const int rounds = (w1 - w0 + NT - 1) / NT;
+      for (int k = threadIdx.x; k < tops.threads * rounds; k += NT) {
+        const int w = w0 + tops.thread[k / rounds] + k % rounds * NT;
+        if (w >= w1) continue;
+        const uint4 one[1] = {row.load(w)};
+        if (key_of(batch_max<T>(one)) >= bound) {
+          const int at = atomicAdd(&tops.windows, 1);
+          if (at < kCap) tops.window[at] = w;
+        }
+      }
+      __syncthreads();
+      // the elements of those that reach the bound, one per thread
+      const int hits = tops.windows;
+      for (int k = threadIdx.x; k < min(hits, kCap) * N; k += NT) {
+        const int c = row.col(tops.window[k / N]) + k % N;
+        if (c < 0 || c >= row.V) continue;
+        const uint32_t key = key_of(to_f32(row.p[c]));
+        if (key >= bound) {
+          const int at = atomicAdd(&tops.count, 1);
+          if (at < kCap) tops.list[at] = entry(key, c);
+        }
+      }
+      __syncthreads();
+      const int n = hits <= kCap ? tops.count : kCap + 1;
       if (n <= kCap)
-        rank_list<NT>(n, a.top, sm.list, sm.best);
+        rank_list<NT>(n, a.top, tops.list, tops.best);
       else
-        collect_many<T, NT>(row, w0, w1, a.top, bound, mine, sm);
+        collect_many<T, NT>(row, w0, w1, a.top, bound, mine, tops);
       __syncthreads();
     }
 
     if (parts > 1) {
       if (threadIdx.x == 0) {
-        st_first(&sm.all[part].m, __float_as_uint(all.m));
-        st_first(&sm.all[part].s, __float_as_uint(all.s));
-        st_first(&sm.all[part].g, __float_as_uint(all.g));
+        st_first(&sums.all[part].m, __float_as_uint(all.m));
+        st_first(&sums.all[part].s, __float_as_uint(all.s));
+        st_first(&sums.all[part].g, __float_as_uint(all.g));
       }
       if (TOP && threadIdx.x < a.top) {
-        Entry* to = &sm.bests[part * a.top + threadIdx.x];
-        st_first(&to->key, sm.best[threadIdx.x].key);
-        st_first(&to->idx, static_cast<uint32_t>(sm.best[threadIdx.x].idx));
+        const Entry e = tops.best[threadIdx.x];
+        uint32_t* to = reinterpret_cast<uint32_t*>(&tops.bests[part * a.top + threadIdx.x]);
+        st_first(to, static_cast<uint32_t>(e));
+        st_first(to + 1, static_cast<uint32_t>(e >> 32));
       }
       __syncwarp();
       cluster_sync();
       if (part == 0) {
         all = Sums::none();
-        if (lane < parts) all = sm.all[lane];
+        if (lane < parts) all = sums.all[lane];
         all = warp_merge(all, ENT);
         if (TOP) {
-          rank_list<NT>(parts * a.top, a.top, sm.bests, sm.best);
+          rank_list<NT>(parts * a.top, a.top, tops.bests, tops.best);
           __syncthreads();
         }
       }
     }
-    if (part == 0) {
+    if (part == 0 && warp == 0) {
       const bool empty = all.s == 0.0f;   // every logit is -infinity
-      const float ls = logf(all.s), ninf = __uint_as_float(0xFF800000u);
-      if (threadIdx.x == 0) {
-        a.lse[r] = empty ? ninf : all.m + ls;
-        if (a.targets) a.logp[r] = counts ? (empty ? ninf : (zt - all.m) - ls) : 0.0f;
+      const float ls = logf(all.s), none = __uint_as_float(0xFF800000u);
+      if (lane == 0) {
+        a.lse[r] = empty ? none : all.m + ls;
+        if (a.targets) a.logp[r] = counts ? (empty ? none : (zt - all.m) - ls) : 0.0f;
         if (ENT) a.entropy[r] = empty ? 0.0f : ls - all.g / all.s;
       }
-      if (TOP && threadIdx.x < a.top) {
-        const Entry e = sm.best[threadIdx.x];
-        a.top_ids[r * a.top + threadIdx.x] = e.idx;
-        a.top_logp[r * a.top + threadIdx.x] = empty ? ninf : (value_of(e.key) - all.m) - ls;
+      if (TOP && lane < a.top) {
+        const Entry e = tops.best[lane];
+        a.top_ids[r * a.top + lane] = entry_idx(e);
+        a.top_logp[r * a.top + lane] = empty ? none : (value_of(entry_key(e)) - all.m) - ls;
       }
     }
     // the next row's results must not meet this row's readers
     if (parts > 1) {
       __syncwarp();
       cluster_sync();
-    } else {
+    } else if (TOP) {
       __syncthreads();
+    }
+  }
+  cp_async_wait(0);
+}
+
+// ---------------------------------------------------------------------------
+// Backward: 256 threads (or a warp) take 4 windows each of a row at a time.
+// ---------------------------------------------------------------------------
+// lse in fp32 is off by up to 2^-24 |lse|, and p by that as a factor.  Beyond this
+// size (2^-16) the row is measured again, where probabilities would be wrong
+// altogether if a mask of -1e9 or of the type's lowest value left nothing else.
+constexpr float kExactLse = 256.0f;
+
+// What a row's gradient takes: p = exp(z - m) / S, log p = z - m - ls.
+struct RowGrad {
+  float m, ls, inv_s;   // m and ls: lse and 0, or the largest logit and log S
+  float dl, dh, h;      // gradients of logp and entropy, the entropy
+  int64_t t;            // the given token, -1 where it does not count
+};
+
+template <bool ENT>
+__device__ __forceinline__ RowGrad row_grad(const LogpArgs& a, int64_t r) {
+  RowGrad g = {a.lse_in[r], 0.0f, 1.0f, a.dlogp[r], ENT ? a.dentropy[r] : 0.0f, ENT ? a.entropy_in[r] : 0.0f,
+               a.targets[r]};
+  if (g.t < 0 || g.t >= a.V) {
+    g.t = -64;   // in no window, the row's first included
+    g.dl = 0.0f;
+  }
+  // a row of -infinity only: measured from 0, its probabilities come out as 0
+  if (g.m == __uint_as_float(0xFF800000u)) g.m = g.dl = g.dh = 0.0f;
+  return g;
+}
+
+// Gradient of one window (what load() gave for its columns col ..) into `out`;
+// `same`: the window is a 16-byte one of the gradient's row as well.
+template <typename T, bool ENT>
+__device__ __forceinline__ void grad_window(const RowGrad& g, const uint4& v, int col, int V, int cols, bool same, T* out) {
+  constexpr int N = Vec<T>::N;
+  const float unit = -g.inv_s;
+  const f2 minus = f2_dup(-g.m), l2e = f2_dup(kLog2e), along = f2_dup(g.dh * unit),
+           scale = f2_dup((ENT ? fmaf(g.dh, g.h - g.ls, g.dl) : g.dl) * unit);
+  f2 z[N / 2], o[N / 2];
+  unpack2(v, z, T());
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    f2 d = f2_add(z[i], minus);
+    float x0, x1;
+    f2_get(f2_mul(d, l2e), x0, x1);
+    const f2 p = f2_make(ex2(x0), ex2(x1));
+    if (ENT) {
+      f2_get(d, x0, x1);
+      d = f2_make(fmaxf(x0, -1e4f), fmaxf(x1, -1e4f));   // 0 * -infinity counts as 0
+    }
+    o[i] = f2_mul(p, ENT ? f2_fma(d, along, scale) : scale);
+  }
+  if (g.t >= col && g.t < col + N) {
+    const int hit = static_cast<int>(g.t - col);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      float x0, x1;
+      f2_get(o[i], x0, x1);
+      o[i] = f2_make(hit == 2 * i ? x0 + g.dl : x0, hit == 2 * i + 1 ? x1 + g.dl : x1);
+    }
+  }
+  if (same && col >= 0 && col + N <= V) {
+    *reinterpret_cast<uint4*>(out + col) = pack2(o, T());
+  } else {   // zeros past the vocabulary
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float x0, x1;
+      f2_get(o[i / 2], x0, x1);
+      const float x = col + i < V ? (i & 1 ? x1 : x0) : 0.0f;
+      if (col + i >= 0 && col + i < cols) out[col + i] = from_f32<T>(x);
     }
   }
 }
 
-// ---------------------------------------------------------------------------
-// Backward: a CTA takes 256 x 4 windows of a row.
-// ---------------------------------------------------------------------------
-template <typename T, bool ENT>
-__global__ void __launch_bounds__(256) k_logp_bwd(LogpArgs a, int tiles) {
-  constexpr int N = Vec<T>::N;
+// A whole row by its threads (all of the CTA or one warp), measured before any
+// of it is written (the gradient may be in place).
+template <typename T, bool ENT, int TPR>
+__device__ __forceinline__ void grad_large(const Row<T>& row, RowGrad g, int nw, int cols, bool same, T* out) {
+  __shared__ float part[8];
+  const int tid = threadIdx.x % TPR, own = row.windows();
+  float m = kLowest, s = 0.0f;
+#pragma unroll 1
+  for (int w = tid; w < own; w += TPR) {
+    const uint4 one[1] = {row.load(w)};
+    m = fmaxf(m, batch_max<T>(one));
+  }
+  m = warp_max(m);
+  if (TPR > 32) {
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, part[i]);
+  }
+#pragma unroll 1
+  for (int w = tid; w < own; w += TPR) {
+    float z[Row<T>::N];
+    Vec<T>::unpack(row.load(w), z);
+#pragma unroll
+    for (int i = 0; i < Row<T>::N; ++i) s += ex2((z[i] - m) * kLog2e);
+  }
+  s = warp_sum(s);
+  if (TPR > 32) {
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += part[i];
+  } else {
+    __syncwarp();
+  }
+  g.m = m;
+  g.ls = logf(s);
+  g.inv_s = 1.0f / s;
+#pragma unroll 1
+  for (int w = tid; w < nw; w += TPR) grad_window<T, ENT>(g, row.load(w), row.col(w), row.V, cols, same, out);
+}
+
+// TPR threads to a row: 256, or 32 for short rows.
+template <typename T, bool ENT, int TPR>
+__global__ void __launch_bounds__(256, 5) k_logp_bwd(LogpArgs a) {
+  constexpr int N = Vec<T>::N, ROWS = 256 / TPR;
   griddep_launch_dependents();
   griddep_wait();
-  for (int64_t item = blockIdx.x; item < a.N * tiles; item += gridDim.x) {
-    const int64_t r = item / tiles;
-    const int w0 = static_cast<int>(item - r * tiles) * 256 * kBatch + threadIdx.x;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / TPR; r < a.N;
+       r += static_cast<int64_t>(gridDim.x) * ROWS) {
     const Row<T> row(reinterpret_cast<const T*>(a.logits) + r * a.ld, a.V);
     T* out = reinterpret_cast<T*>(a.dlogits) + r * a.ldd;
-    uint4 v[kBatch];
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) v[b] = row.load(w0 + b * 256);
-    const float lse = a.lse_in[r];
-    const int64_t t = a.targets[r];
-    const bool counts = t >= 0 && t < a.V;
-    const bool empty = lse == __uint_as_float(0xFF800000u);
-    const float dl = counts && !empty ? a.dlogp[r] : 0.0f;
-    float dh = 0.0f, base = dl;
-    if (ENT) {
-      dh = empty ? 0.0f : a.dentropy[r];
-      base = fmaf(dh, a.entropy_in[r], dl);
-    }
-    const f2 minus = f2_dup(-lse), l2e = f2_dup(kLog2e), scale = f2_dup(-base), along = f2_dup(-dh);
     // the windows of the gradient's row are those of the logits' row when both
     // start at the same offset from a 16-byte boundary
     const bool same = (reinterpret_cast<uintptr_t>(out) & 15) / sizeof(T) == static_cast<uintptr_t>(row.sh);
+    const int nw = (a.cols + row.sh + N - 1) / N;
+    bool large = false;
+    for (int w0 = blockIdx.y * TPR * kBatch + threadIdx.x % TPR; w0 < nw; w0 += gridDim.y * TPR * kBatch) {
+      uint4 v[kBatch];
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int col = row.col(w0 + b * 256);
-      if (col >= a.cols) continue;
-      f2 z[N / 2];
-      unpack2(v[b], z, T());
-      float o[N];
+      for (int b = 0; b < kBatch; ++b) v[b] = row.load(w0 + b * TPR);
+      const RowGrad g = row_grad<ENT>(a, r);
+      large = fabsf(g.m) > kExactLse;
+      if (large) break;
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        const f2 d = f2_add(z[i], minus);
-        float x0, x1;
-        f2_get(f2_mul(d, l2e), x0, x1);
-        const f2 p = f2_make(ex2(x0), ex2(x1));
-        f2 f = scale;
-        if (ENT) {
-          f2_get(d, x0, x1);
-          f = f2_fma(f2_make(fmaxf(x0, -1e4f), fmaxf(x1, -1e4f)), along, scale);
-        }
-        f2_get(f2_mul(p, f), o[2 * i], o[2 * i + 1]);
-      }
-      const int hit = static_cast<int>(t - col);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (counts && t >= col && hit == i) o[i] += dl;
-        if (empty) o[i] = 0.0f;
-      }
-      if (col + N > a.V) {   // past the vocabulary: zero
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (col + i >= a.V) o[i] = 0.0f;
-      }
-      if (same && col >= 0 && col + N <= a.cols) {
-        *reinterpret_cast<uint4*>(out + col) = Vec<T>::pack(o);
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (col + i >= 0 && col + i < a.cols) out[col + i] = from_f32<T>(o[i]);
+      for (int b = 0; b < kBatch; ++b) {
+        const int col = row.col(w0 + b * TPR);
+        if (col < a.cols) grad_window<T, ENT>(g, v[b], col, a.V, a.cols, same, out);
       }
     }
+    // the first CTA of a row takes it all when it is measured again
+    const bool again = TPR > 32 ? __syncthreads_or(large) : __any_sync(0xFFFFFFFFu, large);
+    if (blockIdx.y == 0 && again) grad_large<T, ENT, TPR>(row, row_grad<ENT>(a, r), nw, a.cols, same, out);
   }
 }
 
@@ -491,10 +702,17 @@ int split_of(int64_t N, int64_t V) {
 
 template <typename T, int NT, bool ENT, bool TOP>
 cudaError_t run_fwd(LogpArgs a, cudaStream_t st) {
-  const int64_t rows = std::min<int64_t>(a.N, int64_t(1) << 27);
+  // two waves of CTAs where each still gets several rows: SMs differ in the
+  // bandwidth they get, and the ones that are ahead take more of the second
+  const int64_t fit = std::max<int64_t>(1, static_cast<int64_t>(num_sms()) * logp_ctas(NT) / a.split);
+  const int64_t rows = std::min<int64_t>(a.N, a.N >= 6 * fit ? 2 * fit : fit);
+  constexpr uint32_t smem = kStages * kBatch * NT * 16 + sizeof(SharedSums) + (TOP ? sizeof(SharedTop) : 0);
+  auto kernel = k_logp_fwd<T, NT, ENT, TOP>;
+  const cudaError_t e = set_smem(kernel, smem);
+  if (e != cudaSuccess) return e;
   ProfScope prof(QLORA_KC_AUX, st);
   const dim3 cluster(static_cast<unsigned>(a.split), 1, 1);
-  return launch_pdl(k_logp_fwd<T, NT, ENT, TOP>, dim3(static_cast<unsigned>(rows * a.split)), dim3(NT), 0, st,
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(rows * a.split)), dim3(NT), smem, st,
                     a.split > 1 ? &cluster : nullptr, a);
 }
 
@@ -504,24 +722,35 @@ cudaError_t pick_fwd(const LogpArgs& a, cudaStream_t st) {
   return a.entropy ? run_fwd<T, NT, true, false>(a, st) : run_fwd<T, NT, false, false>(a, st);
 }
 
+// Threads per row: one batch of windows each for short rows; for long ones 256
+// where that gives every CTA several rows (4096 x 32000 bf16: 52 us, 63 us with
+// 512), 512 where it does not (1024 x 131072 bf16: 53 us, 48 us with 512), and
+// 1024 where there are fewer rows than SMs.
 template <typename T>
 cudaError_t by_size(LogpArgs a, cudaStream_t st) {
   const int64_t windows = a.V / Vec<T>::N;
   a.split = split_of(a.N, a.V);
-  if (windows > 2048 && a.N * a.split <= 2 * num_sms()) return pick_fwd<T, 1024>(a, st);
-  if (windows > 2048) return pick_fwd<T, 512>(a, st);
-  if (windows > 256) return pick_fwd<T, 256>(a, st);
-  return pick_fwd<T, 128>(a, st);
+  for (a.split_log2 = 0; (1 << a.split_log2) < a.split;) ++a.split_log2;
+  if (windows > 1024 && a.N * a.split <= num_sms()) return pick_fwd<T, 1024>(a, st);
+  if (windows > 1024 && a.N < 6 * num_sms() * logp_ctas(256)) return pick_fwd<T, 512>(a, st);
+  if (windows > 1024) return pick_fwd<T, 256>(a, st);
+  if (windows > 32 * kBatch) return pick_fwd<T, 128>(a, st);
+  return pick_fwd<T, 32>(a, st);
 }
 
 template <typename T>
 cudaError_t run_bwd(const LogpArgs& a, cudaStream_t st) {
   const int64_t windows = ceil_div(a.cols + Vec<T>::N - 1, Vec<T>::N);
-  const int tiles = static_cast<int>(ceil_div(windows, 256 * kBatch));
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.N * tiles, int64_t(1) << 30));
   ProfScope prof(QLORA_KC_AUX, st);
-  return a.dentropy ? launch_pdl(k_logp_bwd<T, true>, dim3(grid), dim3(256), 0, st, nullptr, a, tiles)
-                    : launch_pdl(k_logp_bwd<T, false>, dim3(grid), dim3(256), 0, st, nullptr, a, tiles);
+  if (windows <= 1024 && a.N >= 8 * num_sms()) {
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ceil_div(a.N, 8), INT32_MAX)));
+    return a.dentropy ? launch_pdl(k_logp_bwd<T, true, 32>, grid, dim3(256), 0, st, nullptr, a)
+                      : launch_pdl(k_logp_bwd<T, false, 32>, grid, dim3(256), 0, st, nullptr, a);
+  }
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(a.N, INT32_MAX)),
+                  static_cast<unsigned>(std::min<int64_t>(ceil_div(windows, 256 * kBatch), 65535)));
+  return a.dentropy ? launch_pdl(k_logp_bwd<T, true, 256>, grid, dim3(256), 0, st, nullptr, a)
+                    : launch_pdl(k_logp_bwd<T, false, 256>, grid, dim3(256), 0, st, nullptr, a);
 }
 
 }  // namespace

@@ -57,13 +57,16 @@ def token_logprobs(z, targets, top=0):
             out["entropy"][i] = np.log(s) + (e[live] * (m - z[i][live])).sum() / s
         t = int(targets[i])
         if 0 <= t < V:
-            out["logp"][i] = -np.inf if m == -np.inf else z[i, t] - out["lse"][i]
+            # from the maximum, not from lse: beside logits of 1e38 log s would vanish in it
+            out["logp"][i] = -np.inf if m == -np.inf else (z[i, t] - m) - np.log(s)
     if top:
         ids = np.argsort(-(z + 0.0), axis=1, kind="stable")[:, :top]
         out["top_ids"] = ids.astype(np.int32)
         best = np.take_along_axis(z, ids, 1)
+        m = z.max(axis=1, keepdims=True)
         with np.errstate(invalid="ignore"):
-            out["top_logp"] = np.where(best == -np.inf, -np.inf, best - out["lse"][:, None])
+            ls = np.log(np.exp(z - m).sum(axis=1, keepdims=True))
+            out["top_logp"] = np.where(best == -np.inf, -np.inf, (best - m) - ls)
     return out
 
 

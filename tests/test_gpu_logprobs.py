@@ -81,7 +81,7 @@ def check_backward(z, t, V, f, dlogp, dent, dz):
 
 SIZES = [(1, 1, 0), (3, 2, 0), (5, 7, 1), (4, 33, 0), (9, 255, 0), (300, 1000, 0), (7, 2048, 8), (5, 2049, 3), (65, 4097, 0),
          (3, 16384, 0), (2, 16391, 5), (200, 32000, 0), (1, 50001, 7), (33, 50001, 7), (1, 65536, 0), (1, 131072, 0),
-         (9, 131071, 2), (40, 20000, 0), (400, 17000, 1)]
+         (9, 131071, 2), (40, 20000, 0), (400, 17000, 1), (1300, 1003, 2), (1500, 8100, 0)]
 
 
 @pytest.mark.parametrize("N,V,pad", SIZES)
@@ -147,6 +147,64 @@ def test_rows_that_a_mask_leaves_empty_and_single_survivors():
                                        dentropy=torch.ones(4).cuda())
         assert d.isfinite().all() and not d[0].any() and not d[1].any()
         assert d[3, 10] == 1 and d[3, 4999] == -1
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32] if torch.cuda.is_available() else [])
+@pytest.mark.parametrize("V", [700, 9001, 70000])
+def test_logits_of_any_size(dtype, V):
+    """Rows around 1e38 and the type's largest and lowest values, beside ordinary
+    ones, with and without the entropy."""
+    g = torch.Generator().manual_seed(V)
+    z = torch.randn(10, V, generator=g)
+    big = torch.finfo(dtype).max
+    z[0] *= 1e38
+    z[1] = -1e38
+    z[2] = -9.9e37
+    z[3] = -2.5e38
+    z[3, 5] = -2.4e38
+    z[4, 7] = big
+    z[5] = -big
+    z[6] = big
+    z[7, :] = -INF
+    z[7, V - 1] = -big
+    z[8] = -big
+    z[8, 3] = -1.0
+    z[9] = z[9] * 100 - 1e9
+    x = z.to(dtype).cuda()
+    t = torch.tensor([0, 1, 2, 5, 7, 9, V - 1, V - 1, 3, 4]).cuda()
+    for part in (x, x[5:6], x[6:7], x[2:3]) + ((x.repeat(130, 1),) if V == 700 else ()):   # 1300 rows: a warp to each
+        tt = t[:part.shape[0]] if part.shape[0] <= 10 else t.repeat(130)
+        for ent in (False, True):
+            f = Q.qlora_token_logprobs_fwd(part, tt, top=3, entropy=ent)
+            # a draw beyond 3.4 times 1e38 is infinite: its row is NaN throughout
+            odd = (part == INF).any(1)
+            keep = (~odd).cpu().numpy()
+            assert f.lse[odd].isnan().all() and f.logp[odd].isnan().all()
+            zz = part.double().cpu().numpy()[keep]
+            ref = SO.token_logprobs(zz, tt.cpu().numpy()[keep], 3)
+            assert np.array_equal(f.top_ids.cpu().numpy()[keep], ref["top_ids"])
+            lse = f.lse.double().cpu().numpy()[keep]
+            assert np.all(np.abs(lse - ref["lse"]) <= 4 * U * np.abs(ref["lse"]) + 64 * U)
+            got = f.logp.double().cpu().numpy()[keep]
+            # two logits 3.6e38 apart: their difference is -infinity in fp32
+            want = np.where(ref["logp"] < -3.4028235e38, -INF, ref["logp"])
+            assert np.array_equal(np.isinf(got), np.isinf(want))
+            got, want = (np.where(np.isinf(x), 0, x) for x in (got, want))
+            assert np.all(np.abs(got - want) <= 64 * U + 4 * U * (np.abs(want) + 20))
+            if ent:
+                assert np.all(np.abs(f.entropy.double().cpu().numpy()[keep] - ref["entropy"]) <= 64 * U * (2 + ref["entropy"]))
+            dl = torch.ones(part.shape[0]).cuda()
+            for place in (None, part.clone()):
+                src = part if place is None else place
+                d = Q.qlora_token_logprobs_bwd(src, tt, f.lse, dl, entropy=f.entropy, dentropy=dl if ent else None,
+                                               dlogits=place)[~odd]
+                assert d.isfinite().all()
+                # every row's gradient sums to 0 but for the roundings of its entries
+                assert np.all(np.abs(d.double().sum(1).cpu().numpy()) <= 2 * (half(dtype) + 64 * U) * (3 + np.log(V)))
+
+
+def half(dtype):
+    return torch.finfo(dtype).eps / 2
 
 
 @pytest.mark.parametrize("V", [1000, 40000])
