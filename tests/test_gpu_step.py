@@ -1,0 +1,140 @@
+"""One fine-tuning step through the library's operators as they are used together:
+residual add and rms norm -> NF4 linear layer with its adapter -> log
+probabilities of the next tokens -> their gradient -> the layer's backward ->
+the norm's backward -> AdamW over the adapter and the norm's weight.  Run
+eagerly, and captured into a graph that advances a clock; compared with the same
+step in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import step_oracle as SO
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import bit_quantized_lora_02_b200 as Q
+
+BF16 = torch.bfloat16
+M, K, V, PADDED, R, ALPHA = 200, 256, 1003, 1008, 8, 16.0
+
+
+class Step:
+    """Everything a training program keeps: inputs, the quantised head, masters
+    with bf16 copies, gradient buffers and the optimiser's state."""
+
+    def __init__(self, bits, seed=0):
+        g = torch.Generator().manual_seed(seed)
+        self.x = torch.randn(M, K, generator=g).to(BF16).cuda()
+        self.res = torch.randn(M, K, generator=g).to(BF16).cuda()
+        self.t = torch.randint(0, V, (M,), generator=g).cuda()
+        self.t[::17] = -100
+        self.head = (0.05 * torch.randn(PADDED, K, generator=g)).to(BF16).cuda()
+        self.q = Q.nf4_quantize(self.head)
+        masters = [1 + 0.1 * torch.randn(K, generator=g), torch.randn(R, K, generator=g) / 8,
+                   0.01 * torch.randn(PADDED, R, generator=g)]
+        self.p = [m.cuda() for m in masters]
+        self.c = [m.to(BF16) for m in self.p]
+        self.g = [torch.zeros_like(m) for m in self.p]
+        self.opt = Q.qlora_adamw_alloc(self.p, self.g, state_bits=bits, copies=self.c)
+        self.dl = torch.full((M,), -1.0 / M, device="cuda")          # loss = -mean logp
+
+    def forward_backward(self):
+        w, A, B = self.c
+        y, s, _, rstd = Q.qlora_layer_norm_fwd(self.x, w, residual=self.res, rms=True)
+        z, T = Q.qlora_linear_fwd(y, self.q, A, B, ALPHA)
+        f = Q.qlora_token_logprobs_fwd(z, self.t, vocab=V, entropy=True)
+        dz = Q.qlora_token_logprobs_bwd(z, self.t, f.lse, self.dl, vocab=V, dlogits=z)      # in place
+        dy, _, _ = Q.qlora_linear_bwd(dz, y, self.q, A, B, ALPHA, T_save=T, dA=self.g[1], dB=self.g[2])
+        dx, _, _ = Q.qlora_layer_norm_bwd(dy, s, w, None, rstd, rms=True, dweight=self.g[0])
+        return f, dx
+
+
+def reference(st):
+    """Loss and gradients in 64 bits from the same bf16 weights."""
+    W = Q.nf4_dequantize(st.q).double().cpu().numpy()
+    w, A, B = (c.double().cpu().numpy() for c in st.c)
+    s = (st.x.float() + st.res.float()).to(BF16).double().cpu().numpy()
+    y, _, rstd = SO.norm_forward(s, w, None, 1e-5, True)
+    sc = ALPHA / R
+    z = y @ W.T + sc * (y @ A.T) @ B.T
+    t = st.t.cpu().numpy()
+    r = SO.token_logprobs(z[:, :V], t)
+    dz = np.zeros_like(z)
+    dz[:, :V] = SO.token_logprobs_backward(z[:, :V], t, r["lse"], st.dl.cpu().numpy())
+    dy = dz @ W + sc * (dz @ B) @ A
+    dA, dB = sc * (dz @ B).T @ y, sc * dz.T @ (y @ A.T)
+    dx, dw, _ = SO.norm_backward(dy, s, w, None, rstd, None, True)
+    return r, dx, [dw, dA, dB]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_step_against_64_bits(bits):
+    """Each value passes a handful of roundings to bf16 (2^-8 each: S, Y, the
+    logits, their gradient, dY, dX) and products of K = 256 or V = 1003 terms
+    whose errors are independent: 3% of a gradient's norm bounds six of them
+    (6 x 2^-8 = 2.3%); a log probability is off by the logit's own rounding and
+    the input's, 2^-8 (|z| + |lse|) + 2^-7 |y| |w| sqrt(K) of its terms."""
+    st = Step(bits)
+    ref, dx_ref, grads = reference(st)
+    before = [p.clone() for p in st.p]
+    f, dx = st.forward_backward()
+    size = np.abs(ref["lse"]) + 8
+    assert np.all(np.abs(f.logp.double().cpu().numpy() - ref["logp"]) <= 2.0 ** -6 * size)
+    assert np.all(f.logp.cpu().numpy()[::17] == 0)
+    for got, want in zip([dx] + st.g, [dx_ref] + grads):
+        got = got.double().cpu().numpy()
+        assert np.linalg.norm(got - want) <= 0.03 * np.linalg.norm(want)
+    Q.qlora_adamw_step(st.opt, step=1, lr=1e-3, weight_decay=0.01)
+    for p, old, g, c in zip(st.p, before, st.g, st.c):
+        # the first step moves every weight by lr g / (|g| + eps) beside the decay
+        want = old.double() * (1 - 1e-5) - 1e-3 * g.double() / (g.double().abs() + 1e-8)
+        assert ((p.double() - want).abs() <= 1e-3 * 2.0 ** -18 + 2.0 ** -22 * want.abs()).all()
+        assert torch.equal(c, p.to(BF16))
+    assert Q.qlora_device_status() == 0
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_captured_steps_equal_eager_ones(bits):
+    """The whole step in a graph, replayed: bit for bit the eager steps (every
+    kernel sums in a fixed order)."""
+    eager, cap = Step(bits), Step(bits)
+    clock = Q.qlora_adamw_clock(1e-3)
+    warm = Step(bits)
+    warm.forward_backward()                      # kernels loaded before the capture
+    Q.qlora_adamw_step(warm.opt, step=1, lr=1e-3)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        f, dx = cap.forward_backward()
+        Q.qlora_adamw_step(cap.opt, clock=clock, weight_decay=0.01)
+    for t in (1, 2, 3):
+        graph.replay()
+        fe, dxe = eager.forward_backward()
+        Q.qlora_adamw_step(eager.opt, step=t, lr=1e-3, weight_decay=0.01)
+        torch.cuda.synchronize()
+        assert torch.equal(f.logp, fe.logp) and torch.equal(dx, dxe)
+        for a, b in zip(cap.p + cap.c + cap.g, eager.p + eager.c + eager.g):
+            assert torch.equal(a, b)
+    assert clock[1].item() == 3
+
+
+def test_two_streams_at_once():
+    """Two steps on two streams, each with its own tensors, give what each gives
+    alone."""
+    alone = [Step(8, seed) for seed in (1, 2)]
+    want = [s.forward_backward()[1] for s in alone]
+    both = [Step(8, seed) for seed in (1, 2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in both]
+    got = []
+    for s, stream in zip(both, streams):
+        with torch.cuda.stream(stream):
+            got.append(s.forward_backward()[1])
+            Q.qlora_adamw_step(s.opt, step=1, lr=1e-3)
+    for s in alone:
+        Q.qlora_adamw_step(s.opt, step=1, lr=1e-3)
+    torch.cuda.synchronize()
+    for a, b, s, r in zip(got, want, both, alone):
+        assert torch.equal(a, b)
+        assert all(torch.equal(x, y) for x, y in zip(s.p, r.p))
