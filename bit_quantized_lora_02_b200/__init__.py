@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -635,33 +636,40 @@ _NO_CONTEXT = contextlib.nullcontext()
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _enter(dev: torch.device, stream):
+def _enter(dev: int, stream):
     """(raw stream, context for the call's own allocations): the current stream
     of the tensors' device, or the caller's stream, which then also owns what
     the call allocates."""
     if stream is None:
-        return _raw_stream(dev.index), _NO_CONTEXT
-    if stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the call runs on {dev}")
+        return _raw_stream(dev), _NO_CONTEXT
+    if stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, the call runs on cuda:{dev}")
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
-def _want(t: Optional[torch.Tensor], name: str, shape, dtype, dev: torch.device) -> Optional[int]:
+def _want(t: Optional[torch.Tensor], name: str, shape, dtype, dev: int) -> Optional[int]:
     """The address of an argument that must have this shape and dtype, be
-    contiguous and live on ``dev``; None for an absent one."""
+    contiguous and live on CUDA device ``dev`` (-1: the host); None for an
+    absent one."""
     if t is None:
         return None
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         _expect(t, name, shape, dtype)
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the call runs on {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the call runs on {'cpu' if dev < 0 else f'cuda:{dev}'}")
     return t.data_ptr()
 
 
-def _norm_struct(X: torch.Tensor, weight: torch.Tensor, name: str, rms: bool, eps: float) -> QloraNorm:
+@functools.lru_cache(maxsize=256)
+def _norm_desc(M: int, D: int, dt: int, wdt: int, rms: bool, eps: float):
+    return ctypes.byref(QloraNorm(M, D, dt, wdt, rms, eps))
+
+
+def _norm_struct(X: torch.Tensor, weight: torch.Tensor, name: str, rms: bool, eps: float):
     if X.dim() != 2:
         raise ValueError(f"{name}: shape {tuple(X.shape)}, expected (rows, values)")
-    return QloraNorm(X.shape[0], X.shape[1], _dt(X, name), _dt(weight, "weight"), int(bool(rms)), float(eps))
+    M, D = X.shape
+    return _norm_desc(M, D, _dt(X, name), _dt(weight, "weight"), bool(rms), float(eps))
 
 
 def qlora_layer_norm_fwd(X: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -673,7 +681,7 @@ def qlora_layer_norm_fwd(X: torch.Tensor, weight: torch.Tensor, bias: Optional[t
     (Y, S, mean, rstd) for qlora_layer_norm_bwd; S is X without a residual and
     mean is None for rms.  Y and S may be X or residual (in place)."""
     n = _norm_struct(X, weight, "X", rms, eps)
-    shape, dtype, dev, f32 = X.shape, X.dtype, X.device, torch.float32
+    shape, dtype, dev, f32 = X.shape, X.dtype, X.get_device(), torch.float32
     M, D = shape
     if S is not None and residual is None:
         raise ValueError("S goes with residual")
@@ -700,15 +708,17 @@ def qlora_layer_norm_fwd(X: torch.Tensor, weight: torch.Tensor, bias: Optional[t
         if rstd is None:
             rstd = torch.empty(M, dtype=f32, device=dev)
             pr = rstd.data_ptr()
-    _check(lib().qlora_layer_norm_fwd(ctypes.byref(n), pX, pR, pw, pb, pS, pY, pm, pr, raw))
+    _check(lib().qlora_layer_norm_fwd(n, pX, pR, pw, pb, pS, pY, pm, pr, raw))
     return Y, (X if S is None else S), mean, rstd
 
 
-def _norm_workspace(n: QloraNorm, with_dbias: bool, dev: Optional[torch.device] = None) -> int:
+@functools.lru_cache(maxsize=256)
+def _norm_workspace(M: int, D: int, dt: int, with_dbias: bool, dev: int) -> int:
     size = ctypes.c_size_t()
     # the size goes by the SM count of the current device
-    with contextlib.nullcontext() if dev is None or dev.index == torch.cuda.current_device() else torch.cuda.device(dev):
-        _check(lib().qlora_layer_norm_workspace_size(ctypes.byref(n), int(with_dbias), ctypes.byref(size)))
+    with _NO_CONTEXT if dev < 0 or dev == torch.cuda.current_device() else torch.cuda.device(dev):
+        _check(lib().qlora_layer_norm_workspace_size(_norm_desc(M, D, dt, 1, False, 0.0), int(with_dbias),
+                                                     ctypes.byref(size)))
     return size.value
 
 
@@ -716,7 +726,7 @@ def qlora_layer_norm_workspace_size(M: int, D: int, dtype=torch.bfloat16, with_d
     """Bytes of the backward pass's workspace on the current device."""
     if dtype not in _DT:
         raise ValueError(f"dtype {dtype}, expected torch.bfloat16 or torch.float32")
-    return _norm_workspace(QloraNorm(M, D, _DT[dtype], 1, 0, 0.0), with_dbias)
+    return _norm_workspace(M, D, _DT[dtype], bool(with_dbias), torch.cuda.current_device() if torch.cuda.is_available() else -1)
 
 
 def qlora_layer_norm_bwd(dY: torch.Tensor, S: torch.Tensor, weight: torch.Tensor, mean: Optional[torch.Tensor],
@@ -729,7 +739,7 @@ def qlora_layer_norm_bwd(dY: torch.Tensor, S: torch.Tensor, weight: torch.Tensor
     reaches S along the residual stream.  dweight and dbias are fp32; dbias is
     computed with need_dbias or where a tensor for it is given."""
     n = _norm_struct(S, weight, "S", rms, 0.0)
-    shape, dtype, dev, f32 = S.shape, S.dtype, S.device, torch.float32
+    shape, dtype, dev, f32 = S.shape, S.dtype, S.get_device(), torch.float32
     M, D = shape
     if rstd is None or (mean is None and not rms):
         raise ValueError("mean is required" if rstd is not None else "rstd is required")
@@ -740,7 +750,7 @@ def qlora_layer_norm_bwd(dY: torch.Tensor, S: torch.Tensor, weight: torch.Tensor
     pdw, pdb = _want(dweight, "dweight", (D,), f32, dev), _want(dbias, "dbias", (D,), f32, dev)
     _on_cuda(S, "S")
     if workspace is not None:
-        _same_device(dev, workspace=workspace)
+        _same_device(S.device, workspace=workspace)
     raw, own = _enter(dev, stream)
     with own:
         if dX is None:
@@ -753,8 +763,9 @@ def qlora_layer_norm_bwd(dY: torch.Tensor, S: torch.Tensor, weight: torch.Tensor
             dbias = torch.empty(D, dtype=f32, device=dev)
             pdb = dbias.data_ptr()
         if workspace is None:
-            workspace = torch.empty(max(_norm_workspace(n, dbias is not None, dev), 16), dtype=torch.uint8, device=dev)
-    _check(lib().qlora_layer_norm_bwd(ctypes.byref(n), pdY, pS, pw, pm, pr, pdS, pdX, pdw, pdb, workspace.data_ptr(),
+            nws = _norm_workspace(M, D, _DT[dtype], dbias is not None, dev)
+            workspace = torch.empty(max(nws, 16), dtype=torch.uint8, device=dev)
+    _check(lib().qlora_layer_norm_bwd(n, pdY, pS, pw, pm, pr, pdS, pdX, pdw, pdb, workspace.data_ptr(),
                                       _nbytes(workspace), raw))
     return dX, dweight, dbias
 
@@ -770,7 +781,12 @@ class TokenLogprobs:
     top_logp: Optional[torch.Tensor] = None
 
 
-def _logits_struct(logits: torch.Tensor, vocab: Optional[int], top: int) -> QloraLogits:
+@functools.lru_cache(maxsize=256)
+def _logits_desc(N: int, V: int, ld: int, dt: int, top: int):
+    return ctypes.byref(QloraLogits(N, V, ld, dt, top))
+
+
+def _logits_struct(logits: torch.Tensor, vocab: Optional[int], top: int):
     """Rows may lie further apart than they are long; the values of a row are
     neighbours."""
     if logits.dim() != 2:
@@ -782,7 +798,7 @@ def _logits_struct(logits: torch.Tensor, vocab: Optional[int], top: int) -> Qlor
     sr, sc = logits.stride()
     if cols > 1 and sc != 1 or N > 1 and sr < cols:
         raise ValueError(f"logits: strides {(sr, sc)}, expected rows of neighbouring values that do not overlap")
-    return QloraLogits(N, V, sr if N > 1 else cols, _dt(logits, "logits"), int(top))
+    return _logits_desc(N, V, sr if N > 1 else cols, _dt(logits, "logits"), int(top))
 
 
 def qlora_token_logprobs_fwd(logits: torch.Tensor, targets: Optional[torch.Tensor] = None, vocab: Optional[int] = None,
@@ -794,7 +810,7 @@ def qlora_token_logprobs_fwd(logits: torch.Tensor, targets: Optional[torch.Tenso
     entropy of every row and its `top` (up to 32) most probable tokens, equal
     logits by ascending index.  `out`: tensors of an earlier call to write to."""
     l = _logits_struct(logits, vocab, top)
-    N, dev, f32 = logits.shape[0], logits.device, torch.float32
+    N, dev, f32 = logits.shape[0], logits.get_device(), torch.float32
     pt = _want(targets, "targets", (N,), torch.int64, dev)
     if out is not None:
         have = (out.logp is not None, out.entropy is not None, out.top_ids is not None, out.top_logp is not None)
@@ -813,7 +829,7 @@ def qlora_token_logprobs_fwd(logits: torch.Tensor, targets: Optional[torch.Tenso
                                 torch.empty(N, dtype=f32, device=dev) if entropy else None,
                                 torch.empty(N, top, dtype=torch.int32, device=dev) if top > 0 else None,
                                 torch.empty(N, top, dtype=f32, device=dev) if top > 0 else None)
-    _check(lib().qlora_token_logprobs_fwd(ctypes.byref(l), logits.data_ptr(), pt, _ptr(out.logp), out.lse.data_ptr(),
+    _check(lib().qlora_token_logprobs_fwd(l, logits.data_ptr(), pt, _ptr(out.logp), out.lse.data_ptr(),
                                           _ptr(out.entropy), _ptr(out.top_ids), _ptr(out.top_logp), raw))
     return out
 
@@ -826,7 +842,7 @@ def qlora_token_logprobs_bwd(logits: torch.Tensor, targets: torch.Tensor, lse: t
     logp and (with its entropy) entropy.  Columns from `vocab` on get zeros.
     `dlogits` may be the logits themselves (in place)."""
     l = _logits_struct(logits, vocab, 0)
-    (N, cols), dev, f32 = logits.shape, logits.device, torch.float32
+    (N, cols), dev, f32 = logits.shape, logits.get_device(), torch.float32
     for t, name in ((targets, "targets"), (lse, "lse"), (dlogp, "dlogp")):
         if t is None:
             raise ValueError(f"{name} is required")
@@ -836,7 +852,7 @@ def qlora_token_logprobs_bwd(logits: torch.Tensor, targets: torch.Tensor, lse: t
     pd = _want(dlogp, "dlogp", (N,), f32, dev)
     pe, ph = _want(entropy, "entropy", (N,), f32, dev), _want(dentropy, "dentropy", (N,), f32, dev)
     if dlogits is not None:
-        if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape or dlogits.device != dev:
+        if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape or dlogits.get_device() != dev:
             raise ValueError("dlogits must have the logits' shape, dtype and device")
         _logits_struct(dlogits, vocab, 0)
     _on_cuda(logits, "logits")
@@ -844,7 +860,7 @@ def qlora_token_logprobs_bwd(logits: torch.Tensor, targets: torch.Tensor, lse: t
     if dlogits is None:
         with own:
             dlogits = torch.empty(N, cols, dtype=logits.dtype, device=dev)
-    _check(lib().qlora_token_logprobs_bwd(ctypes.byref(l), logits.data_ptr(), pt, pl, pd, pe, ph, dlogits.data_ptr(),
+    _check(lib().qlora_token_logprobs_bwd(l, logits.data_ptr(), pt, pl, pd, pe, ph, dlogits.data_ptr(),
                                           cols, dlogits.stride(0) if N > 1 else cols, raw))
     return dlogits
 
@@ -949,7 +965,7 @@ def qlora_adamw_step(state: AdamWState, step: Optional[int] = None, lr: Optional
     """One AdamW step, in place.  `step` counts from 1; a clock (see
     qlora_adamw_clock) takes the place of `step` and `lr`.  grad_scale: one fp32
     value on the device that multiplies every gradient."""
-    dev = state.device
+    dev = state.device.index
     if (clock is None) == (step is None or lr is None) or (clock is not None and (step is not None or lr is not None)):
         raise ValueError("either step and lr, or a clock")
     scale = _want(grad_scale, "grad_scale", (1,), torch.float32, dev) if grad_scale is not None else None
@@ -968,7 +984,7 @@ def qlora_adamw_state(state: AdamWState, m: Optional[torch.Tensor] = None, v: Op
         if m is not None or v is not None:
             raise ValueError("32-bit moments are not copied: use the returned tensors")
         return state.m, state.v
-    n, dev = state.m.numel(), state.device
+    n, dev = state.m.numel(), state.device.index
     pm, pv = _want(m, "m", (n,), torch.float32, dev), _want(v, "v", (n,), torch.float32, dev)
     raw, own = _enter(dev, stream)
     with own:
