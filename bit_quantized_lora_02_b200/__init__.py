@@ -7,7 +7,9 @@ PyTorch is used for device memory and streams.  There is no fallback: if the
 library is missing or a call fails, a ``QLoRAError`` is raised.
 
 Names follow the C ABI: ``nf4_quantize``, ``nf4_dequantize``,
-``qlora_linear_fwd``, ``qlora_linear_bwd``.
+``qlora_linear_fwd``, ``qlora_linear_bwd``; beside the linear layer, what else a
+fine-tuning step runs: ``qlora_layer_norm_fwd`` / ``_bwd``,
+``qlora_token_logprobs_fwd`` / ``_bwd``, ``qlora_adamw_step``.
 """
 from __future__ import annotations
 
@@ -703,10 +705,10 @@ def qlora_layer_norm_fwd(X: torch.Tensor, weight: torch.Tensor, bias: Optional[t
             S = torch.empty_like(X)
             pS = S.data_ptr()
         if mean is None and not rms:
-            mean = torch.empty(M, dtype=f32, device=dev)
+            mean = torch.empty(M, dtype=f32, device=X.device)
             pm = mean.data_ptr()
         if rstd is None:
-            rstd = torch.empty(M, dtype=f32, device=dev)
+            rstd = torch.empty(M, dtype=f32, device=X.device)
             pr = rstd.data_ptr()
     _check(lib().qlora_layer_norm_fwd(n, pX, pR, pw, pb, pS, pY, pm, pr, raw))
     return Y, (X if S is None else S), mean, rstd
@@ -757,14 +759,14 @@ def qlora_layer_norm_bwd(dY: torch.Tensor, S: torch.Tensor, weight: torch.Tensor
             dX = torch.empty_like(S)
             pdX = dX.data_ptr()
         if dweight is None:
-            dweight = torch.empty(D, dtype=f32, device=dev)
+            dweight = torch.empty(D, dtype=f32, device=S.device)
             pdw = dweight.data_ptr()
         if dbias is None and need_dbias:
-            dbias = torch.empty(D, dtype=f32, device=dev)
+            dbias = torch.empty(D, dtype=f32, device=S.device)
             pdb = dbias.data_ptr()
         if workspace is None:
             nws = _norm_workspace(M, D, _DT[dtype], dbias is not None, dev)
-            workspace = torch.empty(max(nws, 16), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(max(nws, 16), dtype=torch.uint8, device=S.device)
     _check(lib().qlora_layer_norm_bwd(n, pdY, pS, pw, pm, pr, pdS, pdX, pdw, pdb, workspace.data_ptr(),
                                       _nbytes(workspace), raw))
     return dX, dweight, dbias
@@ -823,12 +825,13 @@ def qlora_token_logprobs_fwd(logits: torch.Tensor, targets: Optional[torch.Tenso
     _on_cuda(logits, "logits")
     raw, own = _enter(dev, stream)
     if out is None:
+        on = logits.device
         with own:
-            out = TokenLogprobs(torch.empty(N, dtype=f32, device=dev) if targets is not None else None,
-                                torch.empty(N, dtype=f32, device=dev),
-                                torch.empty(N, dtype=f32, device=dev) if entropy else None,
-                                torch.empty(N, top, dtype=torch.int32, device=dev) if top > 0 else None,
-                                torch.empty(N, top, dtype=f32, device=dev) if top > 0 else None)
+            out = TokenLogprobs(torch.empty(N, dtype=f32, device=on) if targets is not None else None,
+                                torch.empty(N, dtype=f32, device=on),
+                                torch.empty(N, dtype=f32, device=on) if entropy else None,
+                                torch.empty(N, top, dtype=torch.int32, device=on) if top > 0 else None,
+                                torch.empty(N, top, dtype=f32, device=on) if top > 0 else None)
     _check(lib().qlora_token_logprobs_fwd(l, logits.data_ptr(), pt, _ptr(out.logp), out.lse.data_ptr(),
                                           _ptr(out.entropy), _ptr(out.top_ids), _ptr(out.top_logp), raw))
     return out
@@ -859,7 +862,7 @@ def qlora_token_logprobs_bwd(logits: torch.Tensor, targets: torch.Tensor, lse: t
     raw, own = _enter(dev, stream)
     if dlogits is None:
         with own:
-            dlogits = torch.empty(N, cols, dtype=logits.dtype, device=dev)
+            dlogits = torch.empty(N, cols, dtype=logits.dtype, device=logits.device)
     _check(lib().qlora_token_logprobs_bwd(l, logits.data_ptr(), pt, pl, pd, pe, ph, dlogits.data_ptr(),
                                           cols, dlogits.stride(0) if N > 1 else cols, raw))
     return dlogits
@@ -989,10 +992,10 @@ def qlora_adamw_state(state: AdamWState, m: Optional[torch.Tensor] = None, v: Op
     raw, own = _enter(dev, stream)
     with own:
         if m is None:
-            m = torch.empty(n, dtype=torch.float32, device=dev)
+            m = torch.empty(n, dtype=torch.float32, device=state.device)
             pm = m.data_ptr()
         if v is None:
-            v = torch.empty(n, dtype=torch.float32, device=dev)
+            v = torch.empty(n, dtype=torch.float32, device=state.device)
             pv = v.data_ptr()
     _check(lib().qlora_adamw_state_values(n, state.m.data_ptr(), state.m_scale.data_ptr(), state.v.data_ptr(),
                                           state.v_scale.data_ptr(), pm, pv, raw))

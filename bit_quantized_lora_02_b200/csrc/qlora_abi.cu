@@ -1,6 +1,6 @@
 // qlora_abi.cu -- the extern "C" entry points declared in include/qlora.h:
 // argument validation, buffer-size arithmetic, error reporting.  Every compute
-// step runs in the kernels of nf4_quant.cu and qlora_gemm.cu.
+// step runs in the kernels of the other sources.
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -589,6 +589,7 @@ int qlora_layer_norm_fwd(const qlora_norm_t* n, const void* X, const void* R, co
   if (rc) return rc;
   if (n->M == 0) return ok();
   if ((R == nullptr) != (S == nullptr)) return fail(QLORA_ERR_INVALID_ARG, "S goes with R: both or neither");
+  if (S && S == Y) return fail(QLORA_ERR_INVALID_ARG, "S and Y are the same memory");
   if ((rc = check_ptr16(X, "X", true)) || (rc = check_ptr16(R, "R", false)) ||
       (rc = check_ptr16(weight, "weight", true)) || (rc = check_ptr16(bias, "bias", false)) ||
       (rc = check_ptr16(S, "S", false)) || (rc = check_ptr16(Y, "Y", true)) ||

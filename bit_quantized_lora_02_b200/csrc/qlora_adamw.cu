@@ -27,7 +27,10 @@
 // per value, fp32 masters with bf16 copies and 32-bit states 30.  A warp holds one
 // block of 256 values, 8 to a lane, with the loads of the next ones in flight
 // (cp.async: registers cannot hold them as well); the block's maxima are one redux
-// each.
+// each.  128M bf16 parameters with fp32 gradients and 8-bit states: 242 us, the
+// measured rate of a plain copy (103%); 50 instructions per value fill half of the
+// issue slots.  448 adapter tensors (40M values) with fp32 masters, bf16 copies and
+// 32-bit states: 183 us (101%).
 // Tensors, their pointers and the chunk where each starts travel as kernel
 // parameters (up to 28 KB): nothing has to be copied to the device before the
 // launch, and a captured graph keeps them.

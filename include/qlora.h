@@ -341,7 +341,8 @@ typedef struct {
  *     mean = sum(S) / D  (rms: 0),  rstd = 1 / sqrt(sum((S - mean)^2) / D + eps),
  *     Y = (S - mean) rstd weight + bias.
  *   X, R, S, Y : M x D.  R may be NULL; S is written when R is given and must
- *                be NULL otherwise.  Y and S may be X's or R's memory.
+ *                be NULL otherwise.  Y and S may be X's or R's memory, not each
+ *                other's.
  *   weight     : D values.   bias : D values or NULL.
  *   mean, rstd : M fp32 each for qlora_layer_norm_bwd; either may be NULL (mean
  *                is written as 0 for rms).

@@ -62,6 +62,7 @@ def test_norm_refusals_of_the_library(L):
     assert fwd(n(), X=None) == -1 and fwd(n(), w=None) == -1 and fwd(n(), Y=None) == -1
     assert fwd(n(), X=0x1008) == -3 and fwd(n(), Y=0x3002) == -3 and fwd(n(), mean=0x4002) == -3
     assert fwd(n(), R=0x6000) == -1 and fwd(n(), S=0x6000) == -1          # S goes with R
+    assert fwd(n(), R=0x6000, S=0x3000) == -1                             # S and Y in one place
     assert fwd(n(M=0), X=None, Y=None) == 0                                # nothing to do
     size = ctypes.c_size_t()
     assert L.qlora_layer_norm_workspace_size(n(), 0, None) == -1
