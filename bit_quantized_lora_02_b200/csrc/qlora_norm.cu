@@ -80,9 +80,6 @@ struct Rows {
   __device__ __forceinline__ uint4 get(int k, int c, uint32_t stage) const {
     return lds128(slot0 + stage + static_cast<uint32_t>((k * CH + c) * tb * 16));
   }
-  __device__ __forceinline__ void put(int k, int c, uint32_t stage, const uint4& v) const {
-    sts128(slot0 + stage + static_cast<uint32_t>((k * CH + c) * tb * 16), v);
-  }
   // whether element i of window c belongs to the row
   __device__ __forceinline__ bool in(int c, int i) const {
     return ALIGNED ? col(c) < D : (col(c) + i >= 0 && col(c) + i < D);
