@@ -127,6 +127,30 @@ def test_top_with_many_equal_logits(top, V):
             assert torch.equal(f.top_ids.long(), want)
 
 
+@pytest.mark.parametrize("low", [-INF, -1e9, "min"])
+@pytest.mark.parametrize("N,V", [(1, 131072), (3, 50001), (300, 9000), (1300, 4096), (700, 1100), (40, 200)])
+def test_top_under_a_mask(N, V, low):
+    """Rows with 0, 1, 5 or half of their logits outside a mask, some rows without
+    one: the top logits, then masked ones by index."""
+    g = torch.Generator().manual_seed(V)
+    for dtype in (BF16, F32):
+        z = (3 * torch.randn(N, V, generator=g)).to(dtype)
+        fill = torch.finfo(dtype).min if low == "min" else low
+        for r in range(N):
+            left = (5, 1, V // 2, 0, V)[r % 5]
+            if r % 10 == 7:
+                z[r, V // 2:] = fill
+            elif left < V:
+                keep = torch.randperm(V, generator=g)[:left]
+                row = torch.full((V,), fill, dtype=dtype)
+                row[keep] = z[r, keep]
+                z[r] = row
+        x = z.cuda()
+        f = Q.qlora_token_logprobs_fwd(x, top=20, entropy=True)
+        want = torch.sort(x.float() + 0.0, dim=1, descending=True, stable=True).indices[:, :20]
+        assert torch.equal(f.top_ids.long(), want)
+
+
 def test_rows_that_a_mask_leaves_empty_and_single_survivors():
     V = 5000
     z = torch.full((4, V), -INF)
