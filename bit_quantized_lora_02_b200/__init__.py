@@ -811,6 +811,8 @@ def qlora_token_logprobs_fwd(logits: torch.Tensor, targets: Optional[torch.Tenso
     (tokens, columns), the first `vocab` columns of which count; with the
     entropy of every row and its `top` (up to 32) most probable tokens, equal
     logits by ascending index.  `out`: tensors of an earlier call to write to."""
+    if not 0 <= top <= 32:
+        raise ValueError(f"top={top}, expected 0 to 32")
     l = _logits_struct(logits, vocab, top)
     N, dev, f32 = logits.shape[0], logits.get_device(), torch.float32
     pt = _want(targets, "targets", (N,), torch.int64, dev)

@@ -579,7 +579,8 @@ cudaError_t launch(const AdamArgs& a, const Scalars& s, int64_t from, int64_t to
 
 template <int PARAM, typename G, bool EIGHT>
 cudaError_t run(const AdamArgs& a, const Scalars& s, cudaStream_t st) {
-  // few tensors: a launch with few parameters (29 KB of them cost 2 us more)
+  // few tensors: a launch with few parameters (29 KB of them cost a
+  // call 1.1 us more: 14 tensors 6.3 us, 5.2 with the small list)
   constexpr int64_t kMany = 400, kFew = 16;
   if (a.count <= kFew) return launch<PARAM, G, EIGHT, kFew>(a, s, 0, a.count, st);
   for (int64_t at = 0; at < a.count; at += kMany) {

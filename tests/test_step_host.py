@@ -241,3 +241,10 @@ def test_logprobs_oracle():
     ((logp * a).sum() + (ent * b).sum()).backward()
     got = SO.token_logprobs_backward(z.detach().numpy(), t.numpy(), ref["lse"], a.numpy(), ref["entropy"], b.numpy())
     assert np.allclose(got, z.grad.numpy(), atol=1e-12)
+
+
+@pytest.mark.parametrize("top", [-1, 33, (1 << 32) + 2])
+def test_number_of_alternatives_outside_its_range(top):
+    """Refused before anything is allocated for them or their number is cut to 32 bits."""
+    with pytest.raises(ValueError, match="expected 0 to 32"):
+        Q.qlora_token_logprobs_fwd(torch.zeros(4, 64, dtype=BF16), torch.zeros(4, dtype=torch.int64), top=top)
