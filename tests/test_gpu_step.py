@@ -138,3 +138,80 @@ def test_two_streams_at_once():
     for a, b, s, r in zip(got, want, both, alone):
         assert torch.equal(a, b)
         assert all(torch.equal(x, y) for x, y in zip(s.p, r.p))
+
+
+def test_two_threads_at_once():
+    """Calls of two host threads, each on its own stream, do not disturb each other."""
+    import threading
+    g = torch.Generator().manual_seed(5)
+    x, w = torch.randn(33, 1001, generator=g).to(BF16).cuda(), torch.randn(1001, generator=g).cuda()
+    t = torch.arange(33).cuda()
+    want = Q.qlora_layer_norm_fwd(x, w), Q.qlora_token_logprobs_fwd(x, t, top=5, entropy=True)
+    dw = Q.qlora_layer_norm_bwd(x, x, w, want[0][2], want[0][3])[1]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(k):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(100):
+                y, _, mean, rstd = Q.qlora_layer_norm_fwd(x, w, stream=stream)
+                d = Q.qlora_layer_norm_bwd(x, x, w, mean, rstd, stream=stream)[1]
+                f = Q.qlora_token_logprobs_fwd(x, t, top=5 * k, entropy=True, stream=stream)
+            stream.synchronize()
+            assert torch.equal(y, want[0][0]) and torch.equal(d, dw) and torch.equal(f.lse, want[1].lse)
+            assert not k or torch.equal(f.top_ids, want[1].top_ids)
+        except Exception as e:          # a failed assertion included: it belongs to the main thread
+            wrong.append(repr(e))
+    threads = [threading.Thread(target=work, args=(k,)) for k in (0, 1)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong, wrong
+
+
+def test_more_than_2_to_the_31_values():
+    """The last rows (blocks) of tensors whose offsets pass 31 bits are those of the
+    same rows alone; as many rows as take the same variant of the kernel."""
+    n, part = 68000, 5000
+    z = torch.randn(n, 32000, device="cuda", dtype=BF16)
+    assert z.numel() > 1 << 31
+    t = torch.randint(0, 32000, (n,), device="cuda")
+    dl = torch.randn(n, device="cuda")
+    all_, one = (Q.qlora_token_logprobs_fwd(a, b, top=3, entropy=True) for a, b in ((z, t), (z[-part:], t[-part:])))
+    for a, b in zip(vars(all_).values(), vars(one).values()):
+        assert torch.equal(a[-part:], b)
+    d = Q.qlora_token_logprobs_bwd(z[-part:], t[-part:], one.lse, dl[-part:])
+    Q.qlora_token_logprobs_bwd(z, t, all_.lse, dl, dlogits=z)
+    assert torch.equal(z[-part:], d)
+    del z, d
+
+    n = 263000
+    x = torch.randn(n, 8192, device="cuda", dtype=BF16)
+    assert x.numel() > 1 << 31
+    w = torch.randn(8192, device="cuda")
+    y, s, mean, rstd = Q.qlora_layer_norm_fwd(x, w, w, residual=x)
+    tail = Q.qlora_layer_norm_fwd(x[-part:], w, w, residual=x[-part:])
+    for a, b in zip((y, s, mean, rstd), tail):
+        assert torch.equal(a[-part:], b)
+    want = Q.qlora_layer_norm_bwd(y[-part:], s[-part:], w, mean[-part:], rstd[-part:])[0]
+    Q.qlora_layer_norm_bwd(y, s, w, mean, rstd, dX=y)
+    assert torch.equal(y[-part:], want)
+    del x, y, s, want, tail
+
+    n, part = (1 << 31) + 300, 256 * 9 + 44
+    p, g = (torch.randn(n, device="cuda", dtype=BF16) for _ in range(2))
+    small = [p[-part:].clone()], [g[-part:].clone()]
+    big, little = Q.qlora_adamw_alloc([p], [g], 8), Q.qlora_adamw_alloc(*small, 8)
+    for step in (1, 2):
+        for state in (big, little):
+            Q.qlora_adamw_step(state, step=step, lr=1e-2)
+    assert torch.equal(p[-part:], small[0][0])
+    blocks = -(-part // 256)
+    for a, b in ((big.m.view(torch.uint8), little.m.view(torch.uint8)), (big.v, little.v)):
+        assert torch.equal(a[-256 * blocks:], b)
+    assert torch.equal(big.m_scale[-blocks:], little.m_scale) and torch.equal(big.v_scale[-blocks:], little.v_scale)
+    m, v = (a[-256 * blocks:] for a in Q.qlora_adamw_state(big))
+    for a, b in zip((m, v), Q.qlora_adamw_state(little)):
+        assert torch.equal(a, b)
