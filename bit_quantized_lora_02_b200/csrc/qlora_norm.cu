@@ -128,6 +128,8 @@ __device__ __forceinline__ float row_sum(float a, float4* scratch) {
   return a;
 }
 
+constexpr float kLargest = 3.402823466e38f;   // the largest finite fp32 value
+
 // CTAs of nt threads per SM at 128 registers per thread.
 constexpr int norm_ctas(int nt) { return nt <= 512 ? 512 / nt : 1; }
 
@@ -204,83 +206,130 @@ __global__ void __launch_bounds__(MAXT, norm_ctas(MAXT)) k_norm_fwd(NormArgs a) 
       for (int i = 0; i < H; ++i) b[c][i] = 0;
   }
   int stage = 0, buf = 0;
+  float mean = 0.0f;
+  int64_t row = R.row0;
 #pragma unroll 1
-  for (int64_t row = R.row0; row < a.M; row += R.stride) {
-    const int64_t at = row * a.D;
-    const uint32_t here = stage * R.stage_bytes;
-    cp_async_wait(a.stages - 1);
-    f2 v[CH][H];
+  while (true) {
+#pragma unroll 1
+    for (; row < a.M; row += R.stride) {
+      const int64_t at = row * a.D;
+      const uint32_t here = stage * R.stage_bytes;
+      cp_async_wait(a.stages - 1);
+      stage = stage + 1 == a.stages ? 0 : stage + 1;
+      f2 v[CH][H];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) unpack2(R.get(0, c, here), v[c], T());
-    if (a.has_r) {
-      T* s = reinterpret_cast<T*>(a.S) + at;
+      for (int c = 0; c < CH; ++c) unpack2(R.get(0, c, here), v[c], T());
+      if (a.has_r) {
+        T* s = reinterpret_cast<T*>(a.S) + at;
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        f2 q[H];
-        unpack2(R.get(1, c, here), q, T());
+        for (int c = 0; c < CH; ++c) {
+          f2 q[H];
+          unpack2(R.get(1, c, here), q, T());
 #pragma unroll
-        for (int i = 0; i < H; ++i) v[c][i] = f2_add(v[c][i], q[i]);
-        const uint4 packed = pack2(v[c], T());
-        unpack2(packed, v[c], T());
-        store_raw<T, ALIGNED>(s, R.col(c), a.D, packed);
-      }
-    }
-    issue(row + a.stages * R.stride, here);
-    if constexpr (!ALIGNED) {
-      if (R.col(0) < 0) {   // values of the row before
-        float lo, hi;
-#pragma unroll
-        for (int i = 0; i < H; ++i) {
-          f2_get(v[0][i], lo, hi);
-          v[0][i] = f2_make(2 * i < R.sh ? 0.0f : lo, 2 * i + 1 < R.sh ? 0.0f : hi);
+          for (int i = 0; i < H; ++i) v[c][i] = f2_add(v[c][i], q[i]);
+          const uint4 packed = pack2(v[c], T());
+          unpack2(packed, v[c], T());
+          store_raw<T, ALIGNED>(s, R.col(c), a.D, packed);
         }
       }
-    }
-    float mean = 0.0f;
-    if (!a.rms) {
-      f2 sum = 0;
-#pragma unroll
-      for (int c = 0; c < CH; ++c)
-#pragma unroll
-        for (int i = 0; i < H; ++i) sum = f2_add(sum, v[c][i]);
-      mean = row_sum<WARP, MAXW>(f2_sum(sum), scratch[buf]) / static_cast<float>(a.D);
-      buf ^= 1;
-      const f2 minus = f2_dup(-mean);
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-#pragma unroll
-        for (int i = 0; i < H; ++i) v[c][i] = f2_add(v[c][i], minus);
-        if (ALIGNED ? R.bytes(c) == 0 : R.bytes(c) < 16 || R.col(c) < 0) {   // outside the row: no share of the variance
+      issue(row + a.stages * R.stride, here);
+      if constexpr (!ALIGNED) {
+        if (R.col(0) < 0) {   // values of the row before
           float lo, hi;
 #pragma unroll
           for (int i = 0; i < H; ++i) {
-            f2_get(v[c][i], lo, hi);
-            v[c][i] = f2_make(R.in(c, 2 * i) ? lo : 0.0f, R.in(c, 2 * i + 1) ? hi : 0.0f);
+            f2_get(v[0][i], lo, hi);
+            v[0][i] = f2_make(2 * i < R.sh ? 0.0f : lo, 2 * i + 1 < R.sh ? 0.0f : hi);
           }
         }
       }
+      if (!a.rms) {
+        f2 sum = 0;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int i = 0; i < H; ++i) sum = f2_add(sum, v[c][i]);
+        mean = row_sum<WARP, MAXW>(f2_sum(sum), scratch[buf]) / static_cast<float>(a.D);
+        buf ^= 1;
+        const f2 minus = f2_dup(-mean);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+#pragma unroll
+          for (int i = 0; i < H; ++i) v[c][i] = f2_add(v[c][i], minus);
+          if (ALIGNED ? R.bytes(c) == 0 : R.bytes(c) < 16 || R.col(c) < 0) {   // outside the row: no share of the variance
+            float lo, hi;
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+              f2_get(v[c][i], lo, hi);
+              v[c][i] = f2_make(R.in(c, 2 * i) ? lo : 0.0f, R.in(c, 2 * i + 1) ? hi : 0.0f);
+            }
+          }
+        }
+      }
+      f2 sq = 0;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < H; ++i) sq = f2_fma(v[c][i], v[c][i], sq);
+      const float squares = row_sum<WARP, MAXW>(f2_sum(sq), scratch[buf]);
+      buf ^= 1;
+      if (!(squares <= kLargest)) break;   // the same for all of the row's threads
+      const float rstd = 1.0f / sqrtf(squares / static_cast<float>(a.D) + a.eps);
+      if (R.t == 0) {
+        if (a.mean_out) a.mean_out[row] = mean;
+        if (a.rstd_out) a.rstd_out[row] = rstd;
+      }
+      T* y = reinterpret_cast<T*>(a.Y) + at;
+      const f2 scale = f2_dup(rstd);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        f2 o[H];
+#pragma unroll
+        for (int i = 0; i < H; ++i) o[i] = f2_fma(f2_mul(v[c][i], scale), w[c][i], b[c][i]);
+        store_raw<T, ALIGNED>(y, R.col(c), a.D, pack2(o, T()));
+      }
     }
-    f2 sq = 0;
+    if (row >= a.M) break;
+    // A row whose squares pass the range of fp32 (values of 1e17 to 1e19 and more,
+    // by its length), from memory again: squares 2^-192 as large reach at most 2^64,
+    // and what they lose below 2^-149 is no share of their sum.  Infinite again or
+    // NaN: the row holds such a value, and all of it becomes NaN.  Outside the loop
+    // over ordinary rows, which keeps its registers that way: 8192 x 8192 bf16 takes
+    // 88 us with the residual, L2 flushed, as without this part, and 92 with it inside.
+    const T* s = reinterpret_cast<const T*>(a.has_r ? a.S : a.X) + row * a.D;
+    float sq = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < CH; ++c) {
+      float x[2 * H];
+      Vec<T>::unpack(load_raw<T, ALIGNED>(s, R.col(c), a.D), x);
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int i = 0; i < H; ++i) sq = f2_fma(v[c][i], v[c][i], sq);
-    const float rstd = 1.0f / sqrtf(row_sum<WARP, MAXW>(f2_sum(sq), scratch[buf]) / static_cast<float>(a.D) + a.eps);
+      for (int i = 0; i < 2 * H; ++i) {
+        const float d = (x[i] - mean) * 0x1p-96f;
+        if (R.in(c, i)) sq = fmaf(d, d, sq);
+      }
+    }
+    const float squares = row_sum<WARP, MAXW>(sq, scratch[buf]);
     buf ^= 1;
+    const float rstd = squares <= kLargest
+                           ? 0x1p-96f / sqrtf(squares / static_cast<float>(a.D) + a.eps * 0x1p-96f * 0x1p-96f)
+                           : __uint_as_float(0x7FC00000u);
     if (R.t == 0) {
       if (a.mean_out) a.mean_out[row] = mean;
       if (a.rstd_out) a.rstd_out[row] = rstd;
     }
-    T* y = reinterpret_cast<T*>(a.Y) + at;
-    const f2 scale = f2_dup(rstd);
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < CH; ++c) {
-      f2 o[H];
+      float x[2 * H];
+      f2 wl[H], bl[H], o[H];
+      Vec<T>::unpack(load_raw<T, ALIGNED>(s, R.col(c), a.D), x);
+      load_w<2 * H>(a.w, wbf16, R.col(c), a.D, wl);
+      load_w<2 * H>(a.b, wbf16, R.col(c), a.D, bl);
 #pragma unroll
-      for (int i = 0; i < H; ++i) o[i] = f2_fma(f2_mul(v[c][i], scale), w[c][i], b[c][i]);
-      store_raw<T, ALIGNED>(y, R.col(c), a.D, pack2(o, T()));
+      for (int i = 0; i < H; ++i)
+        o[i] = f2_fma(f2_make((x[2 * i] - mean) * rstd, (x[2 * i + 1] - mean) * rstd), wl[i], a.has_b ? bl[i] : 0);
+      store_raw<T, ALIGNED>(reinterpret_cast<T*>(a.Y) + row * a.D, R.col(c), a.D, pack2(o, T()));
     }
-    stage = stage + 1 == a.stages ? 0 : stage + 1;
+    row += R.stride;
   }
   cp_async_wait(0);
 }

@@ -347,7 +347,10 @@ typedef struct {
  *   mean, rstd : M fp32 each for qlora_layer_norm_bwd; either may be NULL (mean
  *                is written as 0 for rms).
  * Sums are fp32; each output is rounded once.  A row with a non-finite value
- * gives NaN in that row's Y and nowhere else. */
+ * gives NaN in all of that row's Y, in its rstd, and nowhere else; so does, without
+ * rms, a row whose sum or whose distance from the mean passes the range of fp32.
+ * Squares may pass it: rows of values up to the largest are normalised as others
+ * are (above 8e37 rstd is subnormal, off by up to 2^-22 of itself). */
 int qlora_layer_norm_fwd(const qlora_norm_t *n, const void *X, const void *R, const void *weight, const void *bias,
                          void *S, void *Y, float *mean, float *rstd, qlora_stream_t stream);
 

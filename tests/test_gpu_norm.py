@@ -223,3 +223,61 @@ def test_captured_and_replayed_on_a_side_stream():
     side.synchronize()
     for p, q in zip(want_f + want_b, f + g):
         assert torch.equal(p, q)
+
+
+# The longest path of additions in a row's sum is 40 values of a thread (rows of
+# 16377 to 16383 values), 5 shuffles and 16 warps: 61; the 1024-thread forward has
+# 16 + 5 + 32.  Both are fewer than the 64 that the tolerances above count.
+@pytest.mark.parametrize("M,D", [(40, 300), (700, 1001), (3, 2049), (40, 8192), (300, 8192), (150, 16381)])
+@pytest.mark.parametrize("dtype,rms,scale", [(BF16, True, 1e20), (F32, True, 1e36), (F32, False, 1e20), (BF16, False, 1e30),
+                                             (BF16, True, 1e36)] if torch.cuda.is_available() else [])
+def test_rows_whose_squares_pass_the_range(M, D, dtype, rms, scale):
+    """Finite rows whose sum of squares is infinite in fp32, beside ordinary ones:
+    the same formula, forward and backward.  rstd is a normal number here (above
+    1e-37), so the tolerances are those of ordinary rows."""
+    X, R, w, b, dY, dS = inputs(M, D, dtype, F32, M + D, True, True)
+    X[::2] = (X[::2].double() * scale).to(dtype)
+    for res in (R, None):
+        Y, S, mean, rstd = Q.qlora_layer_norm_fwd(X, w, bias=b, residual=res, rms=rms)
+        check_forward(X, res, w, b, 1e-5, rms, Y, S, mean, rstd)
+        dX, dw, db = Q.qlora_layer_norm_bwd(dY, S, w, mean, rstd, dS=dS, rms=rms, need_dbias=True)
+        check_backward(dY, S, w, mean, rstd, dS, rms, dX, dw, db)
+
+
+@pytest.mark.parametrize("D", [64, 1001, 8192])
+def test_the_largest_values(D):
+    """+-3e38: rstd is 1 / 3e38, a subnormal number whose half step is 2^-150 /
+    2^-128 = 2^-22 of it; then the product and its rounding to the output."""
+    sign = torch.where(torch.arange(D) % 3 == 1, -1.0, 1.0).cuda()
+    w = torch.ones(D, device="cuda")
+    for dtype in (F32, BF16):
+        X = (3e38 * sign).to(dtype).repeat(5, 1)
+        Y, _, _, rstd = Q.qlora_layer_norm_fwd(X, w, rms=True)
+        want = 1.0 / X[0, 0].double()
+        assert ((rstd.double() - want).abs() <= (2.0 ** -22 + 128 * U) * want).all()
+        assert ((Y.double() - sign).abs() <= 2.0 ** -22 + 128 * U + half(dtype)).all()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("rms", [True, False])
+@pytest.mark.parametrize("M,D", [(300, 1001), (2500, 300), (40, 4096), (300, 8192), (300, 9001)])
+def test_a_row_with_a_non_finite_value_is_nan_throughout(value, rms, M, D):
+    for dtype in (BF16, F32):
+        X, R, w, b, _, _ = inputs(M, D, dtype, F32, 5, True, True)
+        keep = torch.arange(M, device="cuda") != 17
+        for res in (None, R):
+            clean = Q.qlora_layer_norm_fwd(X, w, bias=b, residual=res, rms=rms)[0]
+            bad = X.clone()
+            bad[17, D // 2] = value
+            Y, _, _, rstd = Q.qlora_layer_norm_fwd(bad, w, bias=b, residual=res, rms=rms)
+            assert Y[17].isnan().all() and rstd[17].isnan() and torch.equal(Y[keep], clean[keep])
+
+
+def test_a_row_whose_sum_passes_the_range_is_nan_throughout():
+    """Only with a mean: its sum is fp32."""
+    X = torch.full((3, 1000), 1e30, device="cuda")
+    X[1] = 1e37
+    w = torch.ones(1000, device="cuda")
+    Y = Q.qlora_layer_norm_fwd(X, w, bias=w)[0]
+    assert Y[1].isnan().all() and Y[0].isfinite().all() and Y[2].isfinite().all()
+    assert Q.qlora_layer_norm_fwd(X, w, bias=w, rms=True)[0].isfinite().all()
