@@ -2,7 +2,7 @@
 // Decay Regularization", ICLR 2019) over many tensors at once: the adapters' A
 // and B of every projection.
 //
-//     g  = grad_scale grad
+//     g  = grad_scale grad, held to +-2^60
 //     m' = beta1 m + (1 - beta1) g,   v' = beta2 v + (1 - beta2) g^2
 //     p' = p (1 - lr wd) - lr / (1 - beta1^t) m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
 //
@@ -19,6 +19,10 @@
 //      gradients'; linear steps in its fourth root resolve 1.6% of v at the
 //      block's largest value and still reach down to 2^-32 of it, and a positive v
 //      never becomes 0, which would turn the step into m / eps.
+// g is held to 2^60 because its square has to fit fp32: an infinite v' would stay
+// so, and with 8-bit states its block's with it, and freeze the parameters.  The
+// step does not depend on the gradients' scale, so beside moments of less than 2^60
+// it is that of the gradient as it came.  One that is not finite becomes NaN.
 // p' is computed from m' and v' before they are coded.  Every operation on the
 // way to a stored moment is one fp32 operation rounded on its own (no fused
 // multiply-add), so the states are bit-reproducible from this definition.
@@ -194,6 +198,16 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// g held to +-2^60, NaN where it is not finite (then g * 0 is).  One test for a
+// lane's eight values instead took as long.  128M values, 8-bit states: bf16
+// gradients 236 -> 240 us, fp32 ones 250 as without it; 32-bit states as well.
+__device__ __forceinline__ f2 hold(f2 g) {
+  float lo, hi;
+  f2_get(g, lo, hi);
+  asm("min.xorsign.abs.f32 %0, %0, %1;" : "+f"(lo) : "f"(0x1p60f));
+  asm("min.xorsign.abs.f32 %0, %0, %1;" : "+f"(hi) : "f"(0x1p60f));
+  return f2_fma(g, 0, f2_make(lo, hi));
+}
 // largest of a and two magnitudes, NaN if one is
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float r;
@@ -239,7 +253,7 @@ struct Block {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int q = 2 * j + h;
-        gr[h] = f2_mul(gr[h], gs);
+        gr[h] = hold(f2_mul(gr[h], gs));
         // packed products, but scalar sums: the compiler fuses a packed product
         // into the packed sum behind it, which would round once instead of twice
         float a0, a1, q0, q1, x0, x1;

@@ -417,7 +417,7 @@ int qlora_token_logprobs_bwd(const qlora_logits_t *l, const void *logits, const 
 /* One AdamW step over many tensors at once (Loshchilov and Hutter, "Decoupled
  * Weight Decay Regularization", ICLR 2019), for the adapters that
  * qlora_linear_bwd gives the gradients of:
- *     g  = grad_scale grad
+ *     g  = grad_scale grad, held to +-2^60 (RN32 of the product first)
  *     m' = beta1 m + (1 - beta1) g,   v' = beta2 v + (1 - beta2) g^2
  *     p' = p (1 - lr wd) - lr / (1 - beta1^t) m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
  * with the moments in 32 bits, or in 8 with one fp32 scale each for every block
@@ -460,9 +460,11 @@ typedef struct {
 } qlora_adamw_t;
 
 /* The step over `count` tensors (host array, read during the call only).
- * Tensors must not overlap: a parameter listed twice is a race.  A non-finite
- * gradient spoils its parameter and moments, with 8-bit states the moments of
- * its block of 256. */
+ * Tensors must not overlap: a parameter listed twice is a race.  A gradient that
+ * is not finite (after its scale) makes its parameter and moments NaN, with 8-bit
+ * states the moments of its block of 256.  Finite ones of any size do not: the
+ * step does not depend on the gradients' scale, and holding them to 2^60 keeps
+ * their squares finite. */
 int qlora_adamw_step(const qlora_adamw_t *o, const qlora_adamw_tensor_t *tensors, int64_t count,
                      qlora_stream_t stream);
 

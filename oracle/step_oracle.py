@@ -152,20 +152,32 @@ def adamw_decode(mc, ms, vc, vs):
     return m, t * t
 
 
+LIMIT = 2.0 ** 60       # of a gradient's magnitude: its square stays finite in fp32
+
+
+def adamw_hold(g, limit=LIMIT):
+    """g held to +-limit; NaN where it is not finite."""
+    with np.errstate(invalid="ignore"):
+        return (g if limit is None else np.clip(g, -limit, limit)) + g * g.dtype.type(0)
+
+
 def adamw_moments(m, v, g, beta1, beta2, scale=None):
     """fp32 moments after one step, every product and sum rounded (the values an
     8-bit state encodes)."""
     g = g.astype(_f)
     if scale is not None:
         g = g * _f(scale)
+    g = adamw_hold(g)
     return (m * _f(beta1) + g * _f(1.0 - beta1)), (v * _f(beta2) + (g * g) * _f(1.0 - beta2))
 
 
-def adamw_param(p, m, v, g, step, lr, beta1, beta2, eps, wd, scale=None):
-    """The parameter after one step in 64 bits from the old moments m, v."""
+def adamw_param(p, m, v, g, step, lr, beta1, beta2, eps, wd, scale=None, limit=LIMIT):
+    """The parameter after one step in 64 bits from the old moments m, v (limit
+    None: from the gradient as it is)."""
     p, m, v, g = (np.asarray(x, np.float64) for x in (p, m, v, g))
     if scale is not None:
         g = (g.astype(_f) * _f(scale)).astype(np.float64)
+    g = adamw_hold(g, limit)
     m = beta1 * m + (1 - beta1) * g
     v = beta2 * v + (1 - beta2) * g * g
     mh, vh = m / (1 - beta1 ** step), v / (1 - beta2 ** step)

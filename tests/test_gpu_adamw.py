@@ -251,3 +251,50 @@ def test_eight_bit_states_train_like_thirty_two():
             Q.qlora_adamw_step(st, step=t, lr=2e-2 * 0.98 ** t + 1e-5)
         ends[bits] = (curve * p * p).sum().item()
     assert ends[8] <= 2 * ends[32] + 1e-4 * curve.sum().item()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("scaled", [False, True])
+def test_gradients_whose_squares_pass_the_range(bits, scaled):
+    """Finite gradients up to the largest: the step is the formula's (AdamW's steps
+    do not depend on the gradients' scale, so holding them to 2^60 changes none),
+    the states stay finite, and the neighbours move on in the next steps."""
+    n = 1024 + 100
+    g0 = 1e-3 * torch.randn(n, generator=torch.Generator().manual_seed(1))
+    big = {10: 1e19, 300: 1e20, 301: -3e38, 700: -2.0 ** 64, 1100: 3e38}
+    P, G = [torch.full((n,), 0.5, device="cuda")], [g0.clone().cuda()]
+    st = Q.qlora_adamw_alloc(P, G, state_bits=bits)
+    scale = torch.tensor([0.5], device="cuda") if scaled else None
+    for t in (1, 2, 3, 4):
+        if t == 2:
+            for i, x in big.items():
+                G[0][i] = x
+        if t == 3:
+            G[0].copy_(g0)
+        before = snapshot(st)
+        Q.qlora_adamw_step(st, step=t, lr=1e-3, weight_decay=0.01, grad_scale=scale)
+        check_step(st, before, HYPER, t, None if scale is None else np.float32(0.5))
+        assert all(x.isfinite().all() for x in P + list(Q.qlora_adamw_state(st)))
+        p0, gr, m0, v0 = before[0]
+        if t == 2 and bits == 32:
+            # the formula itself, in 64 bits, without a limit on the gradient: where
+            # |g| > 2^60 the old moments are below 2^-60 of the new ones
+            want, _, _ = SO.adamw_param(p0, m0, v0, gr, t, *HYPER, limit=None)
+            if scale is not None:
+                want, _, _ = SO.adamw_param(p0, m0, v0, gr * 0.5, t, *HYPER, limit=None)
+            assert np.all(np.abs(host(P[0]) - want) <= 32 * U * (np.abs(want - p0) + np.abs(p0)))
+        if t > 2:
+            near = np.arange(256, 512)
+            near = near[(near != 300) & (near != 301)]
+            assert bits == 8 or (host(P[0])[near] != p0[near]).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_a_non_finite_gradient_shows(bits, value):
+    P, G, _ = make([(1024,)], 6)
+    st = Q.qlora_adamw_alloc(P, G, state_bits=bits)
+    G[0][300] = value
+    Q.qlora_adamw_step(st, step=1, lr=1e-3)
+    m, v = Q.qlora_adamw_state(st)
+    assert P[0][300].isnan() and P[0].isnan().sum() == 1 and m[300].isnan() and v[300].isnan()
