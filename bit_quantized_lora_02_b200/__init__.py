@@ -681,7 +681,8 @@ def qlora_layer_norm_fwd(X: torch.Tensor, weight: torch.Tensor, bias: Optional[t
     """S = X + residual; Y = (S - mean) rstd weight + bias over each row of a
     bf16 or fp32 (M, D) tensor (rms: no mean is subtracted).  Returns
     (Y, S, mean, rstd) for qlora_layer_norm_bwd; S is X without a residual and
-    mean is None for rms.  Y and S may be X or residual (in place)."""
+    mean is None for rms.  Y and S may be X or residual (in place); where Y is X
+    and there is no residual, nothing holds S any more, and None is returned."""
     n = _norm_struct(X, weight, "X", rms, eps)
     shape, dtype, dev, f32 = X.shape, X.dtype, X.get_device(), torch.float32
     M, D = shape
@@ -711,7 +712,9 @@ def qlora_layer_norm_fwd(X: torch.Tensor, weight: torch.Tensor, bias: Optional[t
             rstd = torch.empty(M, dtype=f32, device=X.device)
             pr = rstd.data_ptr()
     _check(lib().qlora_layer_norm_fwd(n, pX, pR, pw, pb, pS, pY, pm, pr, raw))
-    return Y, (X if S is None else S), mean, rstd
+    if S is None and (pY != pX or M == 0):
+        S = X
+    return Y, S, mean, rstd
 
 
 @functools.lru_cache(maxsize=256)
@@ -740,6 +743,8 @@ def qlora_layer_norm_bwd(dY: torch.Tensor, S: torch.Tensor, weight: torch.Tensor
     the gradient of X and of the residual alike; dS is the gradient that
     reaches S along the residual stream.  dweight and dbias are fp32; dbias is
     computed with need_dbias or where a tensor for it is given."""
+    if S is None:
+        raise ValueError("S is required (a forward pass with Y = X and no residual overwrites it)")
     n = _norm_struct(S, weight, "S", rms, 0.0)
     shape, dtype, dev, f32 = S.shape, S.dtype, S.get_device(), torch.float32
     M, D = shape

@@ -342,7 +342,8 @@ typedef struct {
  *     Y = (S - mean) rstd weight + bias.
  *   X, R, S, Y : M x D.  R may be NULL; S is written when R is given and must
  *                be NULL otherwise.  Y and S may be X's or R's memory, not each
- *                other's.
+ *                other's.  Without R the backward pass reads X, which it cannot
+ *                where Y took its memory.
  *   weight     : D values.   bias : D values or NULL.
  *   mean, rstd : M fp32 each for qlora_layer_norm_bwd; either may be NULL (mean
  *                is written as 0 for rms).

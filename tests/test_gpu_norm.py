@@ -281,3 +281,16 @@ def test_a_row_whose_sum_passes_the_range_is_nan_throughout():
     Y = Q.qlora_layer_norm_fwd(X, w, bias=w)[0]
     assert Y[1].isnan().all() and Y[0].isfinite().all() and Y[2].isfinite().all()
     assert Q.qlora_layer_norm_fwd(X, w, bias=w, rms=True)[0].isfinite().all()
+
+
+def test_in_place_without_a_residual_leaves_no_input_for_the_backward():
+    X, _, w, b, _, _ = inputs(20, 300, BF16, F32, 3, True, False)
+    want, S, _, _ = Q.qlora_layer_norm_fwd(X, w, bias=b)
+    assert S is X
+    x = X.clone()
+    Y, S, mean, rstd = Q.qlora_layer_norm_fwd(x, w, bias=b, Y=x)
+    assert Y is x and torch.equal(Y, want) and S is None
+    with pytest.raises(ValueError, match="S is required"):
+        Q.qlora_layer_norm_bwd(x, S, w, mean, rstd)
+    empty = X[:0]
+    assert Q.qlora_layer_norm_fwd(empty, w, bias=b)[1] is empty

@@ -248,3 +248,10 @@ def test_number_of_alternatives_outside_its_range(top):
     """Refused before anything is allocated for them or their number is cut to 32 bits."""
     with pytest.raises(ValueError, match="expected 0 to 32"):
         Q.qlora_token_logprobs_fwd(torch.zeros(4, 64, dtype=BF16), torch.zeros(4, dtype=torch.int64), top=top)
+
+
+def test_norm_backward_without_its_input():
+    """What a forward pass in place returns for S when it had no residual."""
+    X, w, s = torch.zeros(4, 64, dtype=BF16), torch.ones(64), torch.zeros(4)
+    with pytest.raises(ValueError, match="S is required"):
+        Q.qlora_layer_norm_bwd(X, None, w, s, s)
