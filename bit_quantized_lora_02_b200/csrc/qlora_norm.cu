@@ -428,6 +428,12 @@ __global__ void __launch_bounds__(MAXT, norm_ctas(MAXT)) k_norm_bwd(NormArgs a) 
 #pragma unroll
       for (int i = 0; i < H; ++i) xh[i] = f2_mul(f2_add(xh[i], minus), scale);
     };
+    // Outside the row xh is -mean rstd, and where that is infinite the sum of g xh
+    // becomes NaN.  But then xh is 0 throughout the row: one value next to the mean
+    // would differ from it by 2^-24 |mean| at least, and rstd stay below
+    // 2^24 sqrt(D) / |mean|.  (Asked here, ahead of the sums, this costs nothing; behind
+    // them 8192 x 8192 bf16 takes 111 us instead of 101.)
+    const bool constant = isinf(mean * rstd) && rstd <= kLargest;
     f2 c1 = 0, c2 = 0;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -436,7 +442,7 @@ __global__ void __launch_bounds__(MAXT, norm_ctas(MAXT)) k_norm_bwd(NormArgs a) 
       if constexpr (DB) weight(c, wl);
 #pragma unroll
       for (int i = 0; i < H; ++i) {
-        // outside the row dY and w are zero, so whatever xh is there adds nothing
+        // outside the row dY and w are zero, so whatever finite xh is there adds nothing
         dw[c][i] = f2_fma(dy[i], xh[i], dw[c][i]);
         if constexpr (DB) db[c][i] = f2_add(db[c][i], dy[i]);
         const f2 g = f2_mul(dy[i], DB ? wl[i] : w[DB ? 0 : c][i]);
@@ -447,6 +453,7 @@ __global__ void __launch_bounds__(MAXT, norm_ctas(MAXT)) k_norm_bwd(NormArgs a) 
     float m1, m2;
     f2_get(row_sum2<WARP, MAXW>(f2_sum(c1), f2_sum(c2), scratch[buf]), m1, m2);
     if (a.dX) {
+      if (constant) m2 = 0.0f;
       const f2 off = f2_dup(a.rms ? 0.0f : -m1 * inv_d), along = f2_dup(-m2 * inv_d);
       T* dx = reinterpret_cast<T*>(a.dX) + row * a.D;
 #pragma unroll

@@ -294,3 +294,21 @@ def test_in_place_without_a_residual_leaves_no_input_for_the_backward():
         Q.qlora_layer_norm_bwd(x, S, w, mean, rstd)
     empty = X[:0]
     assert Q.qlora_layer_norm_fwd(empty, w, bias=b)[1] is empty
+
+
+@pytest.mark.parametrize("D", [1, 4, 64, 100, 128])
+@pytest.mark.parametrize("dtype", [BF16, F32] if torch.cuda.is_available() else [])
+def test_constant_rows_of_huge_values(D, dtype):
+    """xh is 0 throughout a constant row and rstd is 1 / sqrt(eps) = 316, so that
+    mean rstd is infinite; dX is rstd (g - mean g), and nothing of the windows next
+    to the row enters it.  (-1)^r 2^(120 + r) 2^7 stays below 2^128, so mean is exact
+    where D is a power of two; elsewhere the row's own rounding counts as usual."""
+    X = torch.stack([torch.full((D,), (-1.0) ** r * 2.0 ** (118 + r)) for r in range(3)]).to(dtype).cuda()
+    _, _, w, _, dY, _ = inputs(3, D, dtype, F32, 4, False, False)
+    for bias in (False, True):
+        Y, S, mean, rstd = Q.qlora_layer_norm_fwd(X, w, eps=1e-5)
+        dX, dw, db = Q.qlora_layer_norm_bwd(dY, S, w, mean, rstd, need_dbias=bias)
+        assert dX.isfinite().all() and dw.isfinite().all()
+        if D & (D - 1) == 0:
+            assert torch.equal(mean, X[:, 0].float()) and not Y.any() and not dw.any()
+            check_backward(dY, S - mean[:, None].to(dtype), w, mean * 0, rstd, None, False, dX, dw, db)
