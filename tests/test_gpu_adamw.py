@@ -298,3 +298,16 @@ def test_a_non_finite_gradient_shows(bits, value):
     Q.qlora_adamw_step(st, step=1, lr=1e-3)
     m, v = Q.qlora_adamw_state(st)
     assert P[0][300].isnan() and P[0].isnan().sum() == 1 and m[300].isnan() and v[300].isnan()
+
+
+@pytest.mark.parametrize("bits,param,grad,copies", [(32, F32, F32, True), (32, BF16, BF16, False), (8, BF16, F32, False),
+                                                    (8, F32, BF16, True)])
+def test_more_blocks_per_warp_than_its_loads_run_ahead(bits, param, grad, copies):
+    """Four blocks to a warp with 32-bit states (loads one ahead), five with 8-bit
+    ones (three ahead), at 148 SMs; a second tensor starts in a later chunk."""
+    P, G, C = make([(6200 if bits == 32 else 7400, 4096), (777, 1001)], 4, param, grad, copies)
+    st = Q.qlora_adamw_alloc(P, G, state_bits=bits, copies=C)
+    Q.qlora_adamw_step(st, step=1, lr=1e-3, weight_decay=0.01)
+    before = snapshot(st)
+    Q.qlora_adamw_step(st, step=2, lr=1e-3, weight_decay=0.01)
+    check_step(st, before, HYPER, 2)

@@ -334,3 +334,60 @@ def test_captured_reused_outputs_and_a_side_stream():
             for name in ("logp", "lse", "entropy", "top_ids", "top_logp"):
                 assert torch.equal(getattr(r, name), getattr(want, name))
         assert torch.equal(d, grad) and torch.equal(e, grad)
+
+
+def device_reference(z, t, top):
+    """The same definitions in 64 bits as the oracle's, on the device, for shapes
+    that would take the host minutes (finite logits only)."""
+    x = z.double()
+    m = x.amax(1, keepdim=True)
+    e = torch.exp(x - m)
+    s = e.sum(1)
+    lse = m[:, 0] + torch.log(s)
+    counts = (t >= 0) & (t < z.shape[1])
+    zt = x.gather(1, torch.where(counts, t, 0)[:, None])[:, 0]
+    ent = torch.log(s) + (e * (m - x)).sum(1) / s
+    ids = torch.sort(z.float() + 0.0, dim=1, descending=True, stable=True).indices[:, :top]
+    return torch.where(counts, zt - lse, 0.0), lse, ent, ids, x.gather(1, ids) - lse[:, None]
+
+
+# Rows enough that every CTA (or warp) of each variant of the forward walks over
+# three at least, and that its ring of two batches wraps within them, at 148 SMs:
+# 256, 512 and 128 threads and one warp to a row.
+@pytest.mark.parametrize("N,V,pad", [(4000, 9001, 0), (4000, 32000, 0), (1700, 17001, 2), (4000, 5001, 3), (8000, 1000, 0),
+                                     (8000, 509, 3)])
+@pytest.mark.parametrize("dtype", [BF16, F32] if torch.cuda.is_available() else [])
+@pytest.mark.parametrize("top,entropy", [(20, True), (0, True), (0, False), (5, False)])
+def test_many_rows_for_every_variant(N, V, pad, dtype, top, entropy):
+    g = torch.Generator(device="cuda").manual_seed(N + V)
+    z = (3 * torch.randn(N, V + pad, generator=g, device="cuda")).to(dtype)
+    t = torch.randint(0, V, (N,), generator=g, device="cuda")
+    t[1], t[N // 2] = V, -100
+    dl, dh = torch.randn(N, generator=g, device="cuda"), torch.randn(N, generator=g, device="cuda")
+    f = Q.qlora_token_logprobs_fwd(z, t, vocab=V, top=top, entropy=entropy)
+    d = Q.qlora_token_logprobs_bwd(z, t, f.lse, dl, entropy=f.entropy, dentropy=dh if entropy else None, vocab=V)
+    assert not d[:, V:].any()
+    for r in range(0, N, 500):
+        b = slice(r, min(N, r + 500))
+        logp, lse, ent, ids, best = device_reference(z[b, :V], t[b], top)
+        size = lse.abs()
+        assert ((f.lse[b] - lse).abs() <= 64 * U + 2 * U * size).all()
+        assert ((f.logp[b] - logp).abs() <= 64 * U + 2 * U * (2 * size + logp.abs())).all()
+        if entropy:
+            assert ((f.entropy[b] - ent).abs() <= 64 * U * (2 + ent)).all()
+        if top:
+            assert torch.equal(f.top_ids[b].long(), ids)
+            assert ((f.top_logp[b] - best).abs() <= 64 * U + 4 * U * (size[:, None] + best.abs())).all()
+        q = z[b, :V].double() - f.lse[b, None].double()
+        p, counts = torch.exp(q), (t[b] >= 0) & (t[b] < V)
+        w = torch.where(counts, dl[b].double(), 0.0)[:, None]
+        want, weight = -w * p, w.abs().expand_as(p)
+        if entropy:
+            want = want - dh[b, None].double() * p * (q + f.entropy[b, None].double())
+            weight = weight + dh[b, None].double().abs() * (q.abs() + f.entropy[b, None].double())
+        want.scatter_add_(1, torch.where(counts, t[b], 0)[:, None], w)
+        rel = 64 * U + 4 * U * size[:, None] + 4 * U * q.abs()
+        tol = rel * p * weight + 4 * U * want.abs() + 1e-38
+        if dtype == BF16:
+            tol = tol + 2.0 ** -8 * want.abs() * 1.01
+        assert ((d[b, :V].double() - want).abs() <= tol).all()

@@ -312,3 +312,19 @@ def test_constant_rows_of_huge_values(D, dtype):
         if D & (D - 1) == 0:
             assert torch.equal(mean, X[:, 0].float()) and not Y.any() and not dw.any()
             check_backward(dY, S - mean[:, None].to(dtype), w, mean * 0, rstd, None, False, dX, dw, db)
+
+
+# Rows enough that every CTA (or warp) of each variant walks over at least six, two
+# more than the most rows that its loads run ahead, at 148 SMs: a warp to a row
+# with 8, 16 and 32 values to a thread; 32 to 512 threads; 16, 32 and 40 values.
+@pytest.mark.parametrize("M,D", [(13900, 200), (13900, 300), (13900, 511), (13900, 1000), (6900, 2048), (2590, 2049),
+                                 (2590, 4099), (1740, 8192), (870, 8191), (870, 12000), (870, 16381)])
+@pytest.mark.parametrize("dtype,wdtype,rms,bias,residual", [
+    (BF16, F32, True, False, True), (F32, F32, False, True, True), (BF16, BF16, False, True, False),
+    (F32, F32, True, False, False)] if torch.cuda.is_available() else [])
+def test_many_rows_for_every_variant(M, D, dtype, wdtype, rms, bias, residual):
+    X, R, w, b, dY, dS = inputs(M, D, dtype, wdtype, M + D, bias, residual)
+    Y, S, mean, rstd = Q.qlora_layer_norm_fwd(X, w, bias=b, residual=R, rms=rms)
+    check_forward(X, R, w, b, 1e-5, rms, Y, S, mean, rstd)
+    dX, dw, db = Q.qlora_layer_norm_bwd(dY, S, w, mean, rstd, dS=dS, rms=rms, need_dbias=bias)
+    check_backward(dY, S, w, mean, rstd, dS, rms, dX, dw, db)

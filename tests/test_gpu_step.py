@@ -215,3 +215,24 @@ def test_more_than_2_to_the_31_values():
     m, v = (a[-256 * blocks:] for a in Q.qlora_adamw_state(big))
     for a, b in zip((m, v), Q.qlora_adamw_state(little)):
         assert torch.equal(a, b)
+
+
+def test_weight_gradient_of_more_than_2_to_the_31_values():
+    """The sums over all rows, in 64 bits by blocks of rows.  At 148 SMs each of 296
+    CTAs adds 889 rows, the reduction 10 of their sums per thread and 5 more: fewer
+    than 1024 roundings, on terms with 4 of their own."""
+    n, D = 263000, 8192
+    g = torch.Generator(device="cuda").manual_seed(3)
+    s, dy = (torch.randn(n, D, generator=g, device="cuda", dtype=BF16) for _ in range(2))
+    w = torch.ones(D, device="cuda")
+    mean, rstd = 0.1 * torch.randn(n, generator=g, device="cuda"), 0.5 + torch.rand(n, generator=g, device="cuda")
+    _, dw, db = Q.qlora_layer_norm_bwd(dy, s, w, mean, rstd, need_dbias=True, dX=None)
+    want = torch.zeros(4, D, dtype=torch.float64, device="cuda")
+    for at in range(0, n, 10000):
+        b = slice(at, at + 10000)
+        d = dy[b].double()
+        xh = (s[b].double() - mean[b, None].double()) * rstd[b, None].double()
+        size = (s[b].double().abs() + mean[b, None].double().abs()) * rstd[b, None].double()
+        want += torch.stack([(d * xh).sum(0), d.sum(0), (d.abs() * size).sum(0), d.abs().sum(0)])
+    assert ((dw.double() - want[0]).abs() <= 1024 * 2.0 ** -24 * want[2]).all()
+    assert ((db.double() - want[1]).abs() <= 1024 * 2.0 ** -24 * want[3]).all()
