@@ -289,7 +289,7 @@ __device__ __forceinline__ void st_first(void* p, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
 }
 
-constexpr int logp_ctas(int nt) { return nt >= 1024 ? 1 : nt == 32 ? 16 : 1024 / nt; }   // CTAs per SM
+constexpr int logp_ctas(int nt) { return nt >= 1024 ? 1 : nt == 32 ? 16 : 1024 / nt; }   // CTAs per SM, by registers
 constexpr int kStages = 2;       // batches that a thread's loads run ahead (three leave too little L1: 2 to 13% slower)
 
 // CTAs walk over rows gridDim apart; `split` CTAs of a cluster share a row.  The
@@ -713,11 +713,15 @@ int split_of(int64_t N, int64_t V) {
 
 template <typename T, int NT, bool ENT, bool TOP>
 cudaError_t run_fwd(LogpArgs a, cudaStream_t st) {
+  constexpr uint32_t smem = kStages * kBatch * NT * 16 + sizeof(SharedSums) + (TOP ? sizeof(SharedTop) : 0);
+  // what fits on an SM: with alternatives shared memory allows 6 CTAs of 128 threads
+  // and 10 of a warp (a grid of 8 and 16 left a quarter of the CTAs their whole share
+  // for a second wave)
+  constexpr int64_t per_sm = std::min<int64_t>(logp_ctas(NT), 228 * 1024 / (smem + 1024));
   // two waves of CTAs where each still gets several rows: SMs differ in the
   // bandwidth they get, and the ones that are ahead take more of the second
-  const int64_t fit = std::max<int64_t>(1, static_cast<int64_t>(num_sms()) * logp_ctas(NT) / a.split);
+  const int64_t fit = std::max<int64_t>(1, static_cast<int64_t>(num_sms()) * per_sm / a.split);
   const int64_t rows = std::min<int64_t>(a.N, a.N >= 6 * fit ? 2 * fit : fit);
-  constexpr uint32_t smem = kStages * kBatch * NT * 16 + sizeof(SharedSums) + (TOP ? sizeof(SharedTop) : 0);
   auto kernel = k_logp_fwd<T, NT, ENT, TOP>;
   const cudaError_t e = set_smem(kernel, smem);
   if (e != cudaSuccess) return e;
