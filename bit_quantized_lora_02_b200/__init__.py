@@ -850,7 +850,10 @@ def qlora_token_logprobs_bwd(logits: torch.Tensor, targets: torch.Tensor, lse: t
                              stream=None) -> torch.Tensor:
     """Gradient of the logits from the gradients of qlora_token_logprobs_fwd's
     logp and (with its entropy) entropy.  Columns from `vocab` on get zeros.
-    `dlogits` may be the logits themselves (in place)."""
+    `dlogits` may be the logits themselves (in place).  Padded logits are best
+    passed whole, with `vocab`: a slice of their columns has rows that start at
+    other offsets than those of a new gradient tensor, which is then written value
+    by value."""
     l = _logits_struct(logits, vocab, 0)
     (N, cols), dev, f32 = logits.shape, logits.get_device(), torch.float32
     for t, name in ((targets, "targets"), (lse, "lse"), (dlogp, "dlogp")):

@@ -17,7 +17,9 @@
 //
 // Top alternatives without a second pass over memory: the threads' maxima give
 // those of 32 groups of threads, and the top-th largest of these is a bound that
-// at least `top` logits reach (of distinct values about 32 log(32 / (32 - top))).
+// at least `top` logits reach.  (Of random distinct ones about 32 (H(32) - H(32 -
+// top)) do, H the harmonic numbers: drawing by size until `top` of 32 groups are hit;
+// 31 for 20, 130 for 32.)
 // Only threads whose own maximum reaches it have such logits: their windows are
 // shared out over the CTA and loaded again (from L2), those that reach the bound
 // are shared out by element, and a rank count orders the list, equal logits by
@@ -62,7 +64,7 @@ template <>
 __device__ __forceinline__ uint32_t minus_inf_word<__nv_bfloat16>() { return 0xFF80FF80u; }
 
 // A row of V logits seen through aligned 16-byte windows (qlora_vec.cuh);
-// outside the row they read as -infinity.
+// outside the row they count as -infinity.
 template <typename T>
 struct Row {
   static constexpr int N = Vec<T>::N;
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__(NT, logp_ctas(NT)) k_logp_fwd(LogpArgs a) {
           const int w = bw + b * NT + threadIdx.x;
           const uint32_t dst = slot + stage + b * NT * 16;
           if (w < bw1) {
-            // a window that starts in the row before reads that row's end too
+            // a window that starts ahead of the row reads what lies there too
             cp_async16(dst, src + b * NT * N, min(a.V - brow.col(w), N) * static_cast<int>(sizeof(T)));
           } else {
             sts128(dst, make_uint4(ninf, ninf, ninf, ninf));

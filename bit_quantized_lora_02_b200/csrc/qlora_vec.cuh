@@ -3,8 +3,12 @@
 //
 // Windows: a row that starts `sh` elements past a 16-byte boundary is covered
 // by aligned 16-byte windows; window c holds columns c * N - sh + i, i < N.
-// Only a row's first and last window can reach outside [0, cols); they are
-// read and written element by element, so nothing outside the row is touched.
+// Only a row's first and last window can reach outside [0, cols).  They are written
+// element by element, so nothing outside the row ever is.  Loads into registers
+// (load_raw) stay in the row as well; those into shared memory (cp.async) stop at
+// its end, but take a first window from its 16-byte boundary on: up to 14 bytes
+// ahead of the row, in the same aligned 16 bytes as its first element and so in
+// mapped memory, whoever owns them.  Their values are dropped before any use.
 #pragma once
 
 #include <cstdint>

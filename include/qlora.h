@@ -381,7 +381,10 @@ typedef struct {
   int64_t N;       /* rows (tokens), >= 0                                        */
   int64_t V;       /* logits of a row that count (the vocabulary), 1 .. 2^30     */
   int64_t ld;      /* values from one row's start to the next one's, >= V; the   *
-                    * columns past V (a padded vocabulary) are not read          */
+                    * columns past V (a padded vocabulary) do not count.  Where  *
+                    * a row starts off a 16-byte boundary, the bytes between the *
+                    * boundary and its start (padding, or what lies ahead of the *
+                    * logits) may be read; their values have no effect           */
   int32_t dtype;   /* QLORA_DT_* of the logits and of their gradient, aligned to *
                     * their own size                                             */
   int32_t top;     /* alternatives per row, 0 .. 32 and at most V                */
@@ -409,6 +412,9 @@ int qlora_token_logprobs_fwd(const qlora_logits_t *l, const void *logits, const 
  *   dentropy : N fp32 or NULL; needs entropy (else entropy may be NULL).
  *   dlogits  : N rows of `cols` >= V values, `ldd` >= cols apart, written whole
  *              (zeros from column V on).  May be the logits' memory when ldd = ld.
+ *              Fastest where each of its rows starts at the same offset from a
+ *              16-byte boundary as the logits' row: else it is written value by
+ *              value.
  * Rows whose target does not count have dlogp taken as 0; rows of -infinity
  * only get zeros. */
 int qlora_token_logprobs_bwd(const qlora_logits_t *l, const void *logits, const int64_t *targets, const float *lse,
