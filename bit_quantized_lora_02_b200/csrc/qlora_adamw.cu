@@ -31,8 +31,8 @@
 // per value, fp32 masters with bf16 copies and 32-bit states 30.  A warp holds one
 // block of 256 values, 8 to a lane, with the loads of the next ones in flight
 // (cp.async: registers cannot hold them as well); the block's maxima are one redux
-// each.  128M bf16 parameters with fp32 gradients and 8-bit states: 242 us, the
-// measured rate of a plain copy (103%); 50 instructions per value fill half of the
+// each.  128M bf16 parameters with fp32 gradients and 8-bit states: 247 us, the
+// measured rate of a plain copy (101%); 51 instructions per value fill half of the
 // issue slots.  448 adapter tensors (40M values) with fp32 masters, bf16 copies and
 // 32-bit states: 183 us (101%).
 // Tensors, their pointers and the chunk where each starts travel as kernel
@@ -52,7 +52,7 @@ namespace {
 constexpr int kBlock = 256;
 constexpr int kWarps = 4;               // warps of a CTA, one block each at a time
 // Blocks that a warp's loads run ahead.  128M values: with 8-bit states, whose
-// arithmetic takes long, 242 us at three; with 32-bit ones one is enough (564 us
+// arithmetic takes long, 247 us at three; with 32-bit ones one is enough (564 us
 // with fp32 parameters; two and three were 15% slower at some combinations of
 // types, where their rings fill an SM's shared memory).
 template <bool EIGHT>
@@ -199,8 +199,8 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return r;
 }
 // g held to +-2^60, NaN where it is not finite (then g * 0 is).  One test for a
-// lane's eight values instead took as long.  128M values, 8-bit states: bf16
-// gradients 236 -> 240 us, fp32 ones 250 as without it; 32-bit states as well.
+// lane's eight values instead took as long.  It costs 8-bit states 1 to 2% (128M
+// values: fp32 gradients 245 -> 247 us, bf16 ones 240 -> 245), 32-bit ones nothing.
 __device__ __forceinline__ f2 hold(f2 g) {
   float lo, hi;
   f2_get(g, lo, hi);

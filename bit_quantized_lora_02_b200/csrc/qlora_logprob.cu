@@ -26,10 +26,10 @@
 // their index.  Lists that overflow (rows with few distinct values, as under a
 // mask) take `collect_many`.
 //
-// Bound: HBM in the backward pass (read and write once: 4096 x 32000 bf16 in 90 us,
-// 90% of a copy's measured rate; fp32 99%) and in the fp32 forward (2048 x 32000 in
+// Bound: HBM in the backward pass (read and write once: 4096 x 32000 bf16 in 89 us,
+// 92% of a copy's measured rate; fp32 99%) and in the fp32 forward (2048 x 32000 in
 // 41 us, 99%).  In the bf16 forward (4096 x 32000 with the entropy: 51 us back to
-// back, 80%; 57 between other work, outputs allocated) 2 bytes per logit leave
+// back, 80%; 54 with outputs allocated) 2 bytes per logit leave
 // 11 issue slots for each, of which it takes 9, and the exponential's pipe is two
 // thirds busy.  20 alternatives of each of 4096 rows take 30 us more; one row of
 // 131072 takes 5.6 us, with 8 of them 8.8.

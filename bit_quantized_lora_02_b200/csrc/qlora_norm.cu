@@ -14,10 +14,10 @@
 // Bound: HBM.  Every activation is read and written once: the forward keeps a row
 // in registers between its reductions, the backward reads its two inputs a second
 // time from shared memory.  8192 x 8192 bf16, rms with residual (537 MB each way):
-// forward 84 us, the measured rate of a plain copy; backward 94 to 99 us (84 to
-// 89% of it), of which about 5 are the reduction of 296 rows of partial sums.  Without a
-// residual the forward moves half as much and reaches 77% of the rate: then the
-// two barriers of a row's sums show.
+// forward 83 us, the measured rate of a plain copy; backward 93 to 99 us (84 to
+// 90% of it), of which about 5 are the reduction of 296 rows of partial sums.  Without a
+// residual the forward moves half as much: rms 44 us (94%); with a mean and a bias
+// 50 us (84%), where the second barrier of a row's sums shows.
 #include "qlora_device.cuh"
 #include "qlora_internal.h"
 #include "qlora_vec.cuh"
@@ -547,7 +547,8 @@ struct Cfg {
 // takes, up to 8192 values; longer rows always have 512 threads, since an SM
 // holds one such CTA.  (The last case: unaligned rows next to the limit.)  16
 // values per thread where whole warps of 32 each would leave 15% of the CTA's
-// places empty (32768 x 2049 bf16: forward 157 -> 115 us, backward 183 -> 134; at
+// places empty (32768 x 2049 bf16: forward 157 -> 115 us, L2 flushed, 123 with the
+// rare rows' part in the kernel; backward 183 -> 134; at
 // 4400 values, 9% empty, 96 -> 106 and 107 -> 136), and in a backward pass with
 // the bias's gradient, whose sums and weight leave room for too few rows ahead
 // (8192 x 4096 fp32 93 -> 77 us; bf16 16384 x 4096 89 -> 93, up to 2560 faster).  A

@@ -454,7 +454,8 @@ typedef struct {
 typedef struct {
   int32_t param_dtype, grad_dtype; /* QLORA_DT_*, the same for all tensors of a call */
   int32_t state_bits;              /* 32 or 8                                        */
-  double lr, beta1, beta2, eps, weight_decay; /* 0 <= beta < 1, the others >= 0      */
+  double lr, beta1, beta2, eps, weight_decay; /* 0 <= beta < 1, the others >= 0; an  *
+                                    * eps below 2^-126 counts as 0                   */
   int64_t step;                    /* t, counted from 1                              */
   const float *grad_scale;         /* device fp32, or NULL for 1 (a clipping factor, *
                                     * the inverse of a loss scale)                   */
