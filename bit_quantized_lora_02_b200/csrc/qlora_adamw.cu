@@ -198,9 +198,10 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// g held to +-2^60, NaN where it is not finite (then g * 0 is).  One test for a
-// lane's eight values instead took as long.  It costs 8-bit states 1 to 2% (128M
-// values: fp32 gradients 245 -> 247 us, bf16 ones 240 -> 245), 32-bit ones nothing.
+// g held to +-2^60, NaN where it is not finite (then g * 0 is).  It costs 8-bit
+// states 1 to 2% (128M values: fp32 gradients 245 -> 247 us, bf16 ones 240 -> 245),
+// 32-bit ones nothing.  One test for a lane's eight values took as long; a second
+// pass over a block whose largest v' tells of such a gradient took 1 to 4%.
 __device__ __forceinline__ f2 hold(f2 g) {
   float lo, hi;
   f2_get(g, lo, hi);
