@@ -328,3 +328,28 @@ def test_many_rows_for_every_variant(M, D, dtype, wdtype, rms, bias, residual):
     check_forward(X, R, w, b, 1e-5, rms, Y, S, mean, rstd)
     dX, dw, db = Q.qlora_layer_norm_bwd(dY, S, w, mean, rstd, dS=dS, rms=rms, need_dbias=bias)
     check_backward(dY, S, w, mean, rstd, dS, rms, dX, dw, db)
+
+
+@pytest.mark.parametrize("D", [300, 1001, 8192, 16381])
+@pytest.mark.parametrize("rms", [True, False])
+def test_rows_beyond_the_range_in_place(D, rms):
+    """Such rows are read again after their sums: in place they give what they give
+    elsewhere, for the first, the last and neighbouring rows of a CTA."""
+    M = 900
+    X, R, w, b, _, _ = inputs(M, D, BF16, F32, 12, True, True)
+    for r in (0, 1, 5, 148, 296, 444, 592, 898, 899):
+        X[r] = X[r].double().mul(1e25).to(BF16)
+    X[7, 3] = float("inf")
+    for res in (None, R):
+        Y, S, mean, rstd = Q.qlora_layer_norm_fwd(X, w, bias=b, residual=res, rms=rms)
+        keep = torch.arange(M, device="cuda") != 7
+        assert Y[keep].isfinite().all() and Y[7].isnan().all()
+        for y_in_residual in (False, True):
+            x, r = X.clone(), None if res is None else R.clone()
+            if res is None and y_in_residual:
+                continue
+            y, s = (r, x) if y_in_residual else (x, r)
+            Y2, S2, m2, r2 = Q.qlora_layer_norm_fwd(x, w, bias=b, residual=r, rms=rms, Y=y, S=s)
+            for p, q in ((Y, Y2), (S, S2), (mean, m2), (rstd, r2)):
+                assert p is None or q is None or torch.equal(p[keep], q[keep])
+            assert Y2[7].isnan().all() and r2[7].isnan()
